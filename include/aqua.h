@@ -55,7 +55,7 @@ enum aqua_status_code {
   AQUA_ERR_TIMEOUT = -5      /* a bounded device-side wait ran out (reported by aqua_status) */
 };
 
-enum aqua_dtype { AQUA_F32 = 0, AQUA_BF16 = 1 };
+enum aqua_dtype { AQUA_F32 = 0, AQUA_BF16 = 1, AQUA_E4M3 = 2 /* paged cache only */ };
 
 /* Number of int32 control words the cache's `ctrl` buffer must hold. */
 #define AQUA_CTRL_WORDS 16
@@ -319,6 +319,152 @@ AQUA_API int aqua_h2o_update(aqua_cache* cache, const float* scores, const float
  * Errors: AQUA_ERR_ARG for a missing ctrl block or a limit outside the range.
  */
 AQUA_API int aqua_selftest_wait_timeout(aqua_cache* cache, unsigned long long limit_ns, aqua_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache in 8 bits.
+ *
+ * The same attention step over a cache that a server keeps in pages behind a
+ * block table, at half the bytes of bf16: projected keys and values are held
+ * in e4m3 with one f32 scale for each page and KV head (value = code * scale).
+ * The pages describing AQUA have no counterpart; the step itself (projection,
+ * magnitude top-k, sparse-dimension scores, unprojected values) is theirs.
+ *
+ * Lengths and the block table belong to the caller (the server's scheduler):
+ * no entry point below changes them, and each takes the lengths it uses as an
+ * argument.  Slot t of sequence b is slot t % page_size of page
+ * block_table[b][t / page_size].
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Descriptor of a paged cache (host memory owned by the caller; the buffers
+ * are device memory owned by the caller).
+ *
+ *   k_pages [n_pages][Hkv][d_store][page_size]  e4m3  projected keys, DIMENSION-MAJOR
+ *                                        inside a page, so that a decode step reads
+ *                                        only the rows its heads kept
+ *   v_pages [n_pages][Hkv][page_size][d] e4m3  unprojected values, token-major
+ *   k_scale, v_scale [n_pages][Hkv]      f32   positive; aqua_paged_append gives powers
+ *                                        of two.  Not read for pages without tokens.
+ *   block_table [B][max_pages]           int32 page of every page_size tokens; entries
+ *                                        past a sequence's length are not read
+ *   ctrl    [AQUA_CTRL_WORDS]            int32 control words, zero at creation; word 0 is
+ *                                        the sticky status read by aqua_paged_status
+ *   d       128;  1 <= d_store <= d (d_store < d: AQUA-Memory on the keys)
+ *   page_size  16, 32, 64 or 128 tokens
+ *   dtype   AQUA_E4M3
+ *
+ * A page that aqua_paged_append writes must appear once in the table and in one
+ * sequence only; full pages that are only read may be shared (prefixes).
+ *
+ * Device data that the host cannot check is checked by the kernels, which then
+ * record AQUA_ERR_ARG in the status word and touch nothing out of bounds: a
+ * sequence whose length is negative or beyond max_pages * page_size (or beyond
+ * the rotation table) counts as empty; tokens on a page outside [0, n_pages)
+ * are not written, and are left out of the attention.
+ */
+typedef struct aqua_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  int32_t* ctrl;
+  int B, Hkv, d, d_store, page_size, n_pages, max_pages;
+  int dtype;
+} aqua_paged_cache;
+
+/*
+ * Position rotation applied to query and key rows before the projection.
+ *   cos_sin [n_pos][rot_dim] f32: row t holds cos of the rot_dim / 2 angles of
+ *           position t, then their sin (16-byte aligned)
+ *   rot_dim an even number in [2, 128]: the first rot_dim dimensions are rotated
+ *   interleaved = 0 pairs dimension i with i + rot_dim / 2, 1 pairs 2i with 2i + 1:
+ *           (a, b) -> (a cos - b sin, b cos + a sin)
+ */
+typedef struct aqua_rope {
+  const float* cos_sin;
+  int n_pos, rot_dim, interleaved;
+} aqua_rope;
+
+/* As aqua_status, for a paged cache. */
+AQUA_API int aqua_paged_status(const aqua_paged_cache* cache, int* status_out, aqua_stream_t stream);
+
+/*
+ * Append of new keys and values: k~ = rope(k, position) P[g] in f32, first
+ * d_store dimensions; keys and values are then rounded into the pages (e4m3,
+ * nearest even).  The position of a token is its slot in the sequence.
+ *   k_new, v_new  [n_tokens][Hkv][d] io_dtype (AQUA_F32 or AQUA_BF16).
+ *              Tokens are k_stride / v_stride and heads k_head_stride /
+ *              v_head_stride ELEMENTS apart (0: Hkv * d and d), so that slices of
+ *              a fused projection and head-major tensors are given as they are;
+ *              each row of d dense, 16-byte aligned
+ *   start      [B] int32: tokens each sequence holds already (its first new slot)
+ *   cu_new     nullable [B + 1] int32: sequence b's new tokens are rows
+ *              cu_new[b] .. cu_new[b + 1] - 1 (cu_new[B] = n_tokens; runs may be
+ *              empty).  NULL: one new token for each sequence (n_tokens = B).
+ *   P          [Hkv][d][d] f32;  rope  nullable (rows come rotated already)
+ * Scale of a page and head: the smallest power of two s, at least 2^-60, with
+ * |x| <= 448 s for every finite value x appended to it.  A page that holds
+ * tokens already (start[b] inside it) keeps the larger of its own scale and
+ * that, and when it grows the codes it holds are re-coded (multiplied by the
+ * ratio of the scales, nearest even: exact but for values that become
+ * subnormal).  Slots after the appended tokens are left as they were.
+ * Infinities saturate at 448 s, NaN stays NaN.
+ * Appending a run at once or token by token gives the same values but for those
+ * subnormals.  A sequence whose run does not fit (or lies outside the rotation
+ * table, or whose cu_new is not ascending within [0, n_tokens]) is left as it
+ * was and AQUA_ERR_ARG recorded.
+ */
+AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new, const void* v_new, int io_dtype,
+                               long long k_stride, long long k_head_stride, long long v_stride,
+                               long long v_head_stride, int n_tokens, const int32_t* start, const int32_t* cu_new,
+                               const float* P, const aqua_rope* rope, aqua_stream_t stream);
+
+/*
+ * One decode step over the paged cache for every sequence and query head; the
+ * step of aqua_decode_attn with q rotated on the way.  The query of sequence b
+ * stands at position len[b] - 1 and sees slots 0 .. len[b] - 1 (its own key
+ * was appended before).
+ *   len        [B] int32
+ *   q          [B][Hq][d] io_dtype, sequences q_stride and heads q_head_stride
+ *              ELEMENTS apart (0: Hq * d and d)
+ *   k          dimensions kept per query head, 1 <= k <= d_store
+ *   scale      score scale; <= 0 selects 1/sqrt(d)
+ *   out        [B][Hq][d] out_dtype (AQUA_F32 or AQUA_BF16)
+ *   sel_out, qproj_out, lse_out   nullable, as in aqua_decode_attn.  q~ is
+ *              computed in f64 and rounded once to f32; the selection ranks that.
+ *   workspace  device, 256-byte aligned, >= aqua_paged_decode_workspace_size
+ *              bytes, no initialisation.  Calls that may overlap on the GPU need
+ *              a workspace each.
+ * Hq a multiple of Hkv with Hq / Hkv in 1 .. 8.  A sequence of length 0 gets a
+ * zero output and lse = -inf.  Scores, softmax statistics and sums are f32;
+ * queries and probabilities enter the tensor cores as two f16 parts (about 22
+ * bits), codes exactly.
+ */
+AQUA_API size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq);
+AQUA_API int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,
+                                    long long q_stride, long long q_head_stride, const float* P,
+                                    const aqua_rope* rope, int Hq, int k, float scale, void* out, int out_dtype,
+                                    int32_t* sel_out, float* qproj_out, float* lse_out, void* workspace,
+                                    size_t workspace_bytes, aqua_stream_t stream);
+
+/*
+ * Copies sequences out of the pages into a contiguous cache, where the prompt
+ * path (aqua_prefill_attn) and the other entry points read them.  Sequence
+ * i of dst receives the len[s] tokens of paged sequence s = seq_idx[i] (s = i
+ * when seq_idx is NULL, which needs dst->B = cache->B); every code times its
+ * scale is exact in bf16 for scales that are powers of two.  dst->len and
+ * dst->n_abs (when given) receive the length, dst->max_len becomes max_len;
+ * slots past the length are left as they were.
+ *   len      [cache->B] int32;  seq_idx  nullable [dst->B] int32
+ *   max_len  host bound of the copied lengths, <= dst->Tcap.  A sequence that is
+ *            longer, or an index outside [0, cache->B), counts as empty and
+ *            records AQUA_ERR_ARG in the paged cache's status word; tokens on a
+ *            page outside [0, n_pages) become zeros.
+ * Requires equal Hkv, d and d_store, dst->dv_store = 0 and dst->pos = NULL.
+ */
+AQUA_API int aqua_paged_gather(const aqua_paged_cache* cache, const int32_t* len, const int32_t* seq_idx,
+                               aqua_cache* dst, int max_len, aqua_stream_t stream);
 
 #ifdef __cplusplus
 }
