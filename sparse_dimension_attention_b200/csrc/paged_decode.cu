@@ -20,8 +20,8 @@
 // pages with different scales share one accumulator, and what weighs most in O
 // has p = 1.  e4m3 codes are exact in f16; q~ and p enter as two f16 parts
 // (columns 2h and 2h + 1 of the eight-column operand), 22 bits together.
-// A block that ends inside a (b, g) writes (M, l, O); the last of its blocks to
-// arrive merges them in block order, so results do not depend on timing.
+// A block that starts or ends inside a (b, g) writes (M, l, O);
+// paged_merge_kernel adds the parts in block order, so results do not depend on timing.
 //
 // edgentiq, "How AQUA Works", Online Inference: scores on the selected
 // dimensions, softmax, weighted sum of the unprojected values.
@@ -56,13 +56,14 @@ struct DecodeP {
   float* qproj_out;
   float* lse_out;
   // workspace
-  int32_t* counters;     // [n_units] arrivals of partial results
   int32_t* ucount;       // [n_units] kept rows
   uint8_t* ulist;        // [n_units][D] kept rows, see ulist_slot
   uint2* qfrag;          // [n_units][8][NT][32] masked queries, B operand of the score product
   float* qfac;           // [n_units][kMaxG] factor of a head's scores (log2 domain, without the key scale)
-  float* part_ml;        // [2 * blocks][kMaxG][2]
+  float2* part_ml;       // [2 * blocks][kMaxG] (M, l) of a partial result
   float* part_o;         // [2 * blocks][kMaxG][D]
+  int4* split;           // [blocks] block x starts inside unit .x, whose tiles lie in blocks .y ... .z; .w: slot of
+                         // block .y's part; .x < 0: x starts with a unit
 };
 
 // Row r of the union is loaded by threads r % 16 (groups of eight threads), as
@@ -96,37 +97,48 @@ __device__ __forceinline__ void store_out_elem(const DecodeP& p, size_t i, float
     static_cast<float*>(p.out)[i] = v;
 }
 
+// result of a softmax sum: no visible token gives 0 and -inf, NaN stays
+__device__ __forceinline__ float normalised(float O, float L) { return L == 0.f ? 0.f : O / L; }
+__device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -INFINITY : kLn2 * (M + log2f(L)); }
+
 // ============================================================================
 // rotation, projection, top-k
 // ============================================================================
 
-template <typename T>
+// GP: the group size padded to 1, 2, 4 or 8 (rows G .. GP-1 are zeros and never stored).
+template <typename T, int GP>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, DecodeP p, int G, int NT) {
-  __shared__ __align__(16) double qd[kMaxG][D];     // rotated rows; later the ranking keys
-  __shared__ double part[4][kMaxG][D];
-  __shared__ float qs[kMaxG][D];            // raw rows; later the kept q~, 0 elsewhere
+  constexpr int kSlices = kSelThreads / D, kRows = D / kSlices;      // P rows per thread
+  __shared__ __align__(16) double qd[GP][D];       // rotated rows; later the ranking keys
+  __shared__ double part[kSlices][GP][D];
+  __shared__ float qs[GP][D];                      // raw rows; later the kept q~, 0 elsewhere
   float (*raw)[D] = qs;
   uint32_t (*key)[D] = reinterpret_cast<uint32_t (*)[D]>(&qd[0][0]);
-  __shared__ uint32_t kept[kMaxG][4];
-  __shared__ float qmul[kMaxG];
+  __shared__ uint32_t kept[GP][4];
+  __shared__ float qmul[GP];
   __shared__ int urow[D];
   const int u = blockIdx.x, b = u / c.Hkv, g = u % c.Hkv;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int j = tid & 127, sl = tid >> 7;
+  // P is read before the wait on the previous kernel: whatever may still run then does not write it
+  float pr[kRows];
+  {
+    const float* Pg = p.P + (size_t)g * D * D + (size_t)sl * kRows * D + j;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) pr[i] = __ldg(Pg + i * D);
+  }
   pdl_wait();
   pdl_launch_dependents();
   const int len = __ldg(p.len + b);
   bool bad;
   const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
-  if (tid == 0) {
-    p.counters[u] = 0;
-    if (bad) report_arg(c);
-  }
+  if (tid == 0 && bad) report_arg(c);
   const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
-  for (int i = tid; i < G * D; i += kSelThreads)
-    raw[i >> 7][i & 127] = Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127));
+  for (int i = tid; i < GP * D; i += kSelThreads)
+    raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
   __syncthreads();
-  for (int i = tid; i < G * D; i += kSelThreads) {
-    const int hh = i >> 7, j = i & 127;
+  for (int i = tid; i < GP * D; i += kSelThreads) {
+    const int hh = i >> 7;
     double x = raw[hh][j];
     if (p.rope.cs != nullptr && n > 0) {
       const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
@@ -143,43 +155,48 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   }
   __syncthreads();
   {
-    // partial sums over 32 input dims of column j, all heads of the group
-    const int j = tid & 127, sl = tid >> 7;
-    const float* Pg = p.P + (size_t)g * D * D + (size_t)sl * 32 * D + j;
-    double acc[kMaxG];
+    // partial sums over kRows input dims of column j, all heads of the group
+    double acc[GP];
 #pragma unroll
-    for (int hh = 0; hh < kMaxG; ++hh) acc[hh] = 0.0;
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const double x = __ldg(Pg + i * D);
+    for (int hh = 0; hh < GP; ++hh) acc[hh] = 0.0;
 #pragma unroll
-      for (int hh = 0; hh < kMaxG; ++hh)
-        if (hh < G) acc[hh] = fma(x, qd[hh][sl * 32 + i], acc[hh]);
+    for (int i = 0; i < kRows; i += 2) {
+      const double x0 = pr[i], x1 = pr[i + 1];
+#pragma unroll
+      for (int hh = 0; hh < GP; ++hh) {
+        const double2 qv = *reinterpret_cast<const double2*>(&qd[hh][sl * kRows + i]);
+        acc[hh] = fma(x1, qv.y, fma(x0, qv.x, acc[hh]));
+      }
     }
 #pragma unroll
-    for (int hh = 0; hh < kMaxG; ++hh)
-      if (hh < G) part[sl][hh][j] = acc[hh];
+    for (int hh = 0; hh < GP; ++hh) part[sl][hh][j] = acc[hh];
   }
   __syncthreads();
-  for (int i = tid; i < G * D; i += kSelThreads) {
-    const int hh = i >> 7, j = i & 127;
-    const float qt = (float)((part[0][hh][j] + part[1][hh][j]) + (part[2][hh][j] + part[3][hh][j]));
+  for (int i = tid; i < GP * D; i += kSelThreads) {
+    const int hh = i >> 7;
+    double sum = part[0][hh][j];
+#pragma unroll
+    for (int x = 1; x < kSlices; ++x) sum += part[x][hh][j];
+    const float qt = (float)sum;
     qs[hh][j] = qt;
     // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
     key[hh][j] = j < c.m ? min(__float_as_uint(fabsf(qt)), 0x7F800001u) + 1u : 0u;
-    if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G) * D + i] = qt;
+    if (p.qproj_out && hh < G) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G) * D + i] = qt;
   }
   __syncthreads();
-  // dimension j is kept when fewer than k others rank before it (larger, or equal and lower)
-  for (int hh = w >> 2; hh < G; hh += kSelThreads / D) {
-    const int j = tid & 127;
+  // Dimension j is kept when fewer than k others rank before it (larger, or equal and lower).  Four
+  // warps a head count the larger ones; equal keys are looked at only if they straddle the cut.
+  for (int hh = sl; hh < G; hh += kSlices) {
     const uint32_t kj = key[hh][j];
     int rank = 0;
 #pragma unroll 8
     for (int x = 0; x < D; x += 4) {
       const uint4 o = *reinterpret_cast<const uint4*>(&key[hh][x]);
-      rank += (o.x > kj || (o.x == kj && x + 0 < j)) + (o.y > kj || (o.y == kj && x + 1 < j)) +
-              (o.z > kj || (o.z == kj && x + 2 < j)) + (o.w > kj || (o.w == kj && x + 3 < j));
+      rank += (int)(o.x > kj) + (int)(o.y > kj) + (int)(o.z > kj) + (int)(o.w > kj);
+    }
+    const int in = named_bar_popc(2 + sl, D, j < c.m && rank < p.k);
+    if (in > p.k) {
+      for (int x = 0; x < j; ++x) rank += key[hh][x] == kj;
     }
     const uint32_t bal = __ballot_sync(0xffffffffu, j < c.m && rank < p.k);
     if (lane == 0) kept[hh][w & 3] = bal;
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   __syncthreads();
   // masked rows, their selected dims, and each head's power-of-two normaliser
   for (int i = tid; i < G * D; i += kSelThreads) {
-    const int hh = i >> 7, j = i & 127, wd = j >> 5;
+    const int hh = i >> 7, wd = j >> 5;
     const uint32_t word = kept[hh][wd];
     if ((word >> (j & 31)) & 1u) {
       if (p.sel_out) {
@@ -320,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   __shared__ float merge_ml[kWarps][kMaxG][2];
   __shared__ long long scan[kWarps + 1];
   __shared__ Cursor s_cur;
-  __shared__ int s_last;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
 
   // ---- this block's share [t0, t1) of the flat tile sequence (the lengths were written before the
@@ -338,7 +354,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   }
   total *= c.Hkv;
   const long long nb = min((long long)gridDim.x, total);      // every share has a tile
-  if (blockIdx.x >= nb) return;
+  if (blockIdx.x >= nb) {
+    if (tid == 0) p.split[blockIdx.x].x = -1;
+    return;
+  }
   const long long t0 = blockIdx.x * total / nb, t1 = (blockIdx.x + 1) * total / nb;
   // the unit that holds tile t0
   {
@@ -374,7 +393,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     }
     __syncthreads();
   }
-  pdl_wait();                               // the selection's results
+  pdl_wait();                               // the selection's results; the merge of an earlier call has read its parts
+  pdl_launch_dependents();
+  if (tid == 0) {
+    int4 sp = make_int4(-1, 0, 0, 0);
+    if (s_cur.tile > 0) {
+      // the unit's tiles are [f, f + n) of the flat sequence; tile x lies in block ((x + 1) nb - 1) / total
+      const long long f = t0 - s_cur.tile, n = n_tiles(s_cur.len);
+      const long long first = ((f + 1) * nb - 1) / total, last = ((f + n) * nb - 1) / total;
+      sp = make_int4(s_cur.u, (int)first, (int)last, first * total / nb < f ? 1 : 0);
+    }
+    p.split[blockIdx.x] = sp;
+  }
 
   const int lc = tid & 7, lr = tid >> 3;    // this thread's chunk and first row of every copied tile
   const uint32_t smem0 = smem_u32(dyn);
@@ -626,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       }
     }
     __syncthreads();
-    const int ntile = n_tiles(cc.len);
     const bool whole = seg_start == 0 && last_tile;
     const size_t row0 = (size_t)cc.b * p.Hq + (size_t)cc.g * G;
     const int slot = 2 * blockIdx.x + (it + 1 - (cc.tile + 1 - seg_start) > 0 ? 1 : 0);   // 0: the share's first piece
@@ -643,47 +672,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
         O = fmaf(merge_o[((size_t)x * G + hh) * D + tid], f, O);
       }
       if (whole) {
-        store_out_elem(p, (row0 + hh) * D + tid, L > 0.f ? O / L : (L == 0.f ? 0.f : L));
-        if (p.lse_out && tid == 0) p.lse_out[row0 + hh] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+        store_out_elem(p, (row0 + hh) * D + tid, normalised(O, L));
+        if (p.lse_out && tid == 0) p.lse_out[row0 + hh] = lse_of(M, L);
       } else {
         p.part_o[((size_t)slot * kMaxG + hh) * D + tid] = O;
-        if (tid == 0) {
-          p.part_ml[((size_t)slot * kMaxG + hh) * 2] = M;
-          p.part_ml[((size_t)slot * kMaxG + hh) * 2 + 1] = L;
-        }
-      }
-    }
-    if (!whole) {
-      // blocks of this unit: the tiles [f, f + ntile) of the flat sequence
-      const long long f = t0 + it - cc.tile;
-      const int c0 = (int)(((f + 1) * nb - 1) / total), c1 = (int)(((f + ntile) * nb - 1) / total);
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        s_last = atom_add_acq_rel_gpu(p.counters + cc.u, 1) == c1 - c0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        for (int hh = 0; hh < G; ++hh) {
-          float M = -INFINITY;
-          for (int x = c0; x <= c1; ++x) {
-            const int sl = 2 * x + (x == c0 && x * total / nb < f ? 1 : 0);
-            M = fmaxf(M, __ldcg(p.part_ml + ((size_t)sl * kMaxG + hh) * 2));
-          }
-          const float ref = M == -INFINITY ? 0.f : M;
-          float L = 0.f, O = 0.f;
-#pragma unroll 4
-          for (int x = c0; x <= c1; ++x) {
-            const int sl = 2 * x + (x == c0 && x * total / nb < f ? 1 : 0);
-            const float* ml = p.part_ml + ((size_t)sl * kMaxG + hh) * 2;
-            const float fx = fast_exp2(__ldcg(ml) - ref);
-            L = fmaf(__ldcg(ml + 1), fx, L);
-            O = fmaf(__ldcg(p.part_o + ((size_t)sl * kMaxG + hh) * D + tid), fx, O);
-          }
-          store_out_elem(p, (row0 + hh) * D + tid, L > 0.f ? O / L : (L == 0.f ? 0.f : L));
-          if (p.lse_out && tid == 0) p.lse_out[row0 + hh] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
-        }
+        if (tid == 0) p.part_ml[(size_t)slot * kMaxG + hh] = make_float2(M, L);
       }
     }
     __syncthreads();                        // the merge buffers are free again
@@ -695,9 +688,72 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   cp_async_wait<0>();
 }
 
+// ============================================================================
+// merge of the parts of units that several blocks shared
+// ============================================================================
+
+// One block per (boundary between two attention blocks, query head of the group);
+// the first boundary inside a unit merges it.  Each of eight warps adds every
+// eighth part, a float4 of O per lane, then the eight sums are added in order.
+constexpr int kMergeWarps = 8;
+constexpr int kMaxParts = 2048;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
+  __shared__ float fac[kMaxParts];
+  __shared__ __align__(16) float sum[kMergeWarps][D];
+  __shared__ float red[2][kMergeWarps];
+  const int x = blockIdx.x + 1, hh = blockIdx.y, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  const int4 sp = p.split[x];
+  if (sp.x < 0 || sp.y != x - 1) return;
+  const int n = sp.z - sp.y + 1;
+  auto slot = [&](int i) { return (size_t)(2 * (sp.y + i) + (i == 0 ? sp.w : 0)) * kMaxG + hh; };
+  float M = -INFINITY;
+  for (int i = tid; i < n; i += kMergeWarps * 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][w] = M;
+  __syncthreads();
+#pragma unroll
+  for (int y = 0; y < kMergeWarps; ++y) M = fmaxf(M, red[0][y]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int i = tid; i < n; i += kMergeWarps * 32) {
+    const float2 ml = p.part_ml[slot(i)];
+    const float f = fast_exp2(ml.x - ref);
+    fac[i] = f;
+    L = fmaf(ml.y, f, L);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[1][w] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int y = 0; y < kMergeWarps; ++y) L += red[1][y];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = w; i < n; i += kMergeWarps) {
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * lane);
+    const float f = fac[i];
+    acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+  }
+  *reinterpret_cast<float4*>(&sum[w][4 * lane]) = acc;
+  __syncthreads();
+  if (tid < D) {
+    float O = 0.f;
+#pragma unroll
+    for (int y = 0; y < kMergeWarps; ++y) O += sum[y][tid];
+    const size_t row = (size_t)(sp.x / c.Hkv) * p.Hq + (size_t)(sp.x % c.Hkv) * G + hh;
+    store_out_elem(p, row * D + tid, normalised(O, L));
+    if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(M, L);
+  }
+}
+
 // ---------------------------------------------------------------- host side
 struct Layout {
-  size_t counters, ucount, ulist, qfrag, qfac, part_ml, part_o, total;
+  size_t ucount, ulist, qfrag, qfac, part_ml, part_o, split, total;
 };
 
 Layout layout_of(int n_units, int G, int blocks) {
@@ -709,18 +765,30 @@ Layout layout_of(int n_units, int G, int blocks) {
     return r;
   };
   Layout y;
-  y.counters = take((size_t)n_units * 4);
   y.ucount = take((size_t)n_units * 4);
   y.ulist = take((size_t)n_units * D);
   y.qfrag = take((size_t)n_units * 8 * NT * 32 * sizeof(uint2));
   y.qfac = take((size_t)n_units * kMaxG * 4);
-  y.part_ml = take((size_t)2 * blocks * kMaxG * 2 * 4);
+  y.part_ml = take((size_t)2 * blocks * kMaxG * sizeof(float2));
   y.part_o = take((size_t)2 * blocks * kMaxG * D * 4);
+  y.split = take((size_t)blocks * sizeof(int4));
   y.total = at;
   return y;
 }
 
-int attend_blocks() { return kCtasPerSm * device_sm_count(); }
+int attend_blocks() {
+  const int n = kCtasPerSm * device_sm_count();
+  return n < kMaxParts ? n : kMaxParts;
+}
+
+template <typename T>
+cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NT, cudaStream_t st) {
+  const dim3 grid(c.B * c.Hkv), block(kSelThreads);
+  if (G == 1) return launch_pdl(paged_select_kernel<T, 1>, grid, block, 0, st, c, p, G, NT);
+  if (G == 2) return launch_pdl(paged_select_kernel<T, 2>, grid, block, 0, st, c, p, G, NT);
+  if (G <= 4) return launch_pdl(paged_select_kernel<T, 4>, grid, block, 0, st, c, p, G, NT);
+  return launch_pdl(paged_select_kernel<T, 8>, grid, block, 0, st, c, p, G, NT);
+}
 
 template <int NT>
 int launch_attend(const PagedView& c, const DecodeP& p, int G, int blocks, cudaStream_t st) {
@@ -745,22 +813,22 @@ int launch_paged_decode(const PagedView& c, const int32_t* len, const void* q, b
   DecodeP p;
   p.len = len; p.q = q; p.qs = qs; p.P = P; p.rope = rope; p.Hq = Hq; p.k = k; p.scale = scale;
   p.out = out; p.out_bf16 = out_bf16; p.sel_out = sel_out; p.qproj_out = qproj_out; p.lse_out = lse_out;
-  p.counters = reinterpret_cast<int32_t*>(base + y.counters);
   p.ucount = reinterpret_cast<int32_t*>(base + y.ucount);
   p.ulist = base + y.ulist;
   p.qfrag = reinterpret_cast<uint2*>(base + y.qfrag);
   p.qfac = reinterpret_cast<float*>(base + y.qfac);
-  p.part_ml = reinterpret_cast<float*>(base + y.part_ml);
+  p.part_ml = reinterpret_cast<float2*>(base + y.part_ml);
+  p.split = reinterpret_cast<int4*>(base + y.split);
   p.part_o = reinterpret_cast<float*>(base + y.part_o);
-  cudaError_t e;
-  if (bf16)
-    e = launch_pdl(paged_select_kernel<__nv_bfloat16>, dim3(n_units), dim3(kSelThreads), 0, st, c, p, G, NT);
-  else
-    e = launch_pdl(paged_select_kernel<float>, dim3(n_units), dim3(kSelThreads), 0, st, c, p, G, NT);
+  cudaError_t e = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NT, st) : launch_select<float>(c, p, G, NT, st);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
-  const int rc = check_launch("paged_select_kernel");
+  int rc = check_launch("paged_select_kernel");
   if (rc != AQUA_OK) return rc;
-  return NT == 1 ? launch_attend<1>(c, p, G, blocks, st) : launch_attend<2>(c, p, G, blocks, st);
+  rc = NT == 1 ? launch_attend<1>(c, p, G, blocks, st) : launch_attend<2>(c, p, G, blocks, st);
+  if (rc != AQUA_OK || blocks < 2) return rc;
+  e = launch_pdl(paged_merge_kernel, dim3(blocks - 1, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
+  return check_launch("paged_merge_kernel");
 }
 
 }  // namespace aqua
