@@ -6,20 +6,32 @@
 // queries in the layout the tensor cores take them.
 //
 // paged_attend_kernel, persistent: the tokens of all (b, g) are cut into tiles
-// of 128 and the flat sequence of tiles is split evenly over the blocks.  Per
-// tile the |U| kept key rows (16 tokens a chunk, from whatever page holds them)
-// and the value rows are gathered into shared memory, several tiles ahead; each
-// of the four warps owns 32 tokens and keeps a running softmax of its own:
+// of 128 and the flat sequence of tiles is split evenly over the blocks.
 //
-//   s_t  = ks(page) sum_{j in U} q~_j code_t[j] / sqrt(d)        S^T = K^T q on mma m16n8k16
-//   w_t  = s_t log2(e) + log2 vs(page),   p_t = 2^(w_t - M),  M the running max of w
-//   O   += p_t code_t[v],                 l += p_t / vs(page)    O^T = V^T p^T on mma m16n8k16
+//   s_t  = ks(page) sum_{j in U} q~_j code_t[j] / sqrt(d)
+//   w_t  = s_t log2(e) + log2 vs(page),   p_t = 2^(w_t - M),  M a lazily raised max of w
+//   O   += p_t code_t[v],                 l += p_t / vs(page)
 //   out  = O / l,   lse = ln2 (M + log2 l)
 //
 // Taking the value scale into the exponent makes O a plain sum over codes, so
 // pages with different scales share one accumulator, and what weighs most in O
-// has p = 1.  e4m3 codes are exact in f16; q~ and p enter as two f16 parts
-// (columns 2h and 2h + 1 of the eight-column operand), 22 bits together.
+// has p near 1.
+//
+// Both products run on tcgen05 (kind::f8f6f4) straight from the codes: a tile's
+// kept key rows [dim][128 tokens] and its value rows [token][128 dims] are each
+// the M-major A operand as they lie in the pages, so no code is ever converted.
+// The B operands are q~ and p as sums of e4m3 parts, 16 times finer each: four
+// parts of q~ and three of p (15 and 11 bits or more) for a bf16 output, six of
+// both (about 24 bits) for an f32 one.
+// N = parts x heads is 16 to 64 columns; a product of 128 x 128 x N reads 16 KB
+// of A, so the columns cost next to nothing.  (Products on mma.sync f16, with
+// every code converted in registers, left the kernel bound by instructions: 73 us
+// for 131072 tokens x 8 heads against 41 us of memory time.)
+//
+// Warps 0-3 own one token a thread: scores from tensor memory, softmax, parts of
+// p to shared memory.  Warp 4 issues the products.  Warps 5-8 gather: key rows
+// and value rows in 16-byte pieces from whatever page holds them, written in the
+// 128-byte swizzle the products read; three tiles of 32 KB, two blocks an SM.
 // A block that starts or ends inside a (b, g) writes (M, l, O);
 // paged_merge_kernel adds the parts in block order, so results do not depend on timing.
 //
@@ -35,10 +47,12 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int TT = 128;                    // tokens per tile
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kCtasPerSm = 2;
+constexpr int kSoftThreads = 128;         // one thread per token of a tile
+constexpr int kMmaWarp = 4, kCopyWarp0 = 5;
+constexpr int kCopyThreads = 128;
+constexpr int kThreads = (kCopyWarp0 + kCopyThreads / 32) * 32;
+constexpr int kStages = 3;                // the copies of a tile are announced after those of the next are issued, and
+                                          // S(t + 1) is issued before O(t): two stages would wait on each other
 constexpr int kMaxG = 8;
 constexpr int kSelThreads = 512;
 
@@ -55,10 +69,11 @@ struct DecodeP {
   int32_t* sel_out;
   float* qproj_out;
   float* lse_out;
+  int32_t* ctrl;
   // workspace
   int32_t* ucount;       // [n_units] kept rows
   uint8_t* ulist;        // [n_units][D] kept rows, see ulist_slot
-  uint2* qfrag;          // [n_units][8][NT][32] masked queries, B operand of the score product
+  uint8_t* qpart;        // [n_units][N][D] e4m3 parts of the masked queries: row h * parts + i, columns in union order
   float* qfac;           // [n_units][kMaxG] factor of a head's scores (log2 domain, without the key scale)
   float2* part_ml;       // [2 * blocks][kMaxG] (M, l) of a partial result
   float* part_o;         // [2 * blocks][kMaxG][D]
@@ -75,19 +90,6 @@ __device__ __forceinline__ int n_tiles(int len) { return (len + TT - 1) / TT; }
 __device__ __forceinline__ int seq_tokens(const PagedView& c, const DecodeP& p, int b) {
   bool bad;
   return checked_len(__ldg(p.len + b), c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
-}
-
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 __device__ __forceinline__ void store_out_elem(const DecodeP& p, size_t i, float v) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -I
 
 // GP: the group size padded to 1, 2, 4 or 8 (rows G .. GP-1 are zeros and never stored).
 template <typename T, int GP>
-__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, DecodeP p, int G, int NT) {
+__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, DecodeP p, int G, int NH, int stride, int parts) {
   constexpr int kSlices = kSelThreads / D, kRows = D / kSlices;      // P rows per thread
   __shared__ __align__(16) double qd[GP][D];       // rotated rows; later the ranking keys
   __shared__ double part[kSlices][GP][D];
@@ -242,32 +244,26 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
     for (int x = 0; x < 4; ++x) mx = fmaxf(mx, finite_abs(qs[w][lane + 32 * x]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 2^-e with mx = f 2^e: the largest part lies in [1, 2), far from f16's ends
+    // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
     const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
     if (lane == 0) {
-      qmul[w] = __uint_as_float((uint32_t)(127 - e) << 23);
-      p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale * kLog2e;
+      qmul[w] = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
     }
   }
   __syncthreads();
-  // B operand of the score product: column 2h holds the high and 2h + 1 the low f16 part of head h;
-  // k index 2t + e of a step of 16 rows is row 4t + e, index 2t + 8 + e row 4t + 2 + e
-  for (int i = tid; i < 8 * NT * 32; i += kSelThreads) {
-    const int ln = i & 31, nt = (i >> 5) % NT, ks = (i >> 5) / NT;
-    const int col = ln >> 2, t = ln & 3, hh = 4 * nt + (col >> 1);
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (hh < G) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = urow[16 * ks + 4 * t + e];
-        if (d >= 0) {
-          const float x = qs[hh][d] * qmul[hh];
-          const float hi = __half2float(__float2half_rn(x));
-          v[e] = (col & 1) ? x - hi : hi;
-        }
-      }
+  // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
+  // most half a step, so 16 times it stays in range)
+  for (int i = tid; i < NH * D; i += kSelThreads) {
+    const int hh = i >> 7, d = urow[j];
+    float x = hh < G && d >= 0 ? qs[hh][d] * qmul[hh] : 0.f;
+    if (!(fabsf(x) < INFINITY)) x = NAN;      // an infinite query makes its scores NaN, not the largest code
+    uint8_t* dst = p.qpart + ((size_t)u * NH + hh) * stride * D + j;
+    for (int y = 0; y < stride; ++y) {
+      const uint16_t code = y < parts ? f32x2_to_e4m3x2(x, 0.f) : (uint16_t)0;
+      dst[y * D] = (uint8_t)code;
+      x = (x - e4m3x2_to_f32x2(code).x) * 16.f;
     }
-    p.qfrag[(((size_t)u * 8 + ks) * NT + nt) * 32 + ln] = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
   }
   // an empty sequence has no tiles: attention over no token is 0 with lse -inf
   if (n == 0) {
@@ -281,16 +277,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
 // attention
 // ============================================================================
 
-// Shared memory of one stage: the tile's key rows, its value rows, its scales.
-constexpr int kStageV = D * TT;                       // bytes of V ahead of the key rows
-struct TileMeta {
-  int pid[TT / 16];        // page of every 16 tokens, -1: none
-  float ks[TT / 16];       // its key scale; negative: no page
-  float vs[TT / 16];
-};
-// A tile's page ids are staged one step before its copies are issued, kStages - 1
-// tiles ahead of the one being consumed: kStages + 1 sets are live at once.
-constexpr int kMeta = kStages + 1;
+constexpr int kStageV = D * TT;                       // bytes of a tile's value rows, ahead of its key rows
 
 // Position in the flat sequence of tiles.
 struct Cursor {
@@ -300,9 +287,22 @@ struct Cursor {
   int tile;                // tile of the unit
 };
 
+struct AttendMisc {
+  uint64_t full[kStages], empty[kStages];   // a stage's copies landed / its products are done
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t drain;
+  float ks[kStages][TT / 16];      // key scale of every 16 tokens; negative: their page does not exist
+  float vs[kStages][TT / 16];
+  float red[4][kMaxG];
+  long long scan[kThreads / 32];
+  Cursor cur;
+  uint32_t tmem;
+  int abort;
+};
+
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -314,6 +314,79 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// ------------------------------------------------------------------ tcgen05 wrappers
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// D[tmem] (+)= A[smem] * B[smem], e4m3 in, f32 accumulate
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// 16 consecutive f32 columns of this warp's 32 TMEM lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])),
+      "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
+      "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle, one swizzle atom wide: groups of eight rows of 128
+// bytes, 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(1024 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// kind::f8f6f4: e4m3 A (M-major) and B (K-major), f32 D, 128 x N
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
+}
+
+// Bounded wait that gives up at once when another role did; the first to give up reports.  The copy and
+// softmax threads go on through their loops after that (every later wait returns at once), so that
+// no barrier or shuffle among them is left waiting; what they write then is garbage, in bounds.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* ctrl) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      record_status(ctrl, AQUA_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 // Next unit with tokens after cur (its tiles are used up).
@@ -328,16 +401,36 @@ __device__ __forceinline__ void next_unit(const PagedView& c, const DecodeP& p, 
   } while (cur.b < c.B && cur.len == 0);
   cur.u = cur.b * c.Hkv;
 }
+__device__ __forceinline__ void next_tile(const PagedView& c, const DecodeP& p, Cursor& cur) {
+  if (++cur.tile >= n_tiles(cur.len)) next_unit(c, p, cur);
+}
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(PagedView c, DecodeP p, int G) {
-  extern __shared__ __align__(128) uint8_t dyn[];
-  const int stage_bytes = kStageV + ((c.m + 15) & ~15) * TT;
-  __shared__ TileMeta meta[kMeta];
-  __shared__ float merge_ml[kWarps][kMaxG][2];
-  __shared__ long long scan[kWarps + 1];
-  __shared__ Cursor s_cur;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, gr = lane >> 2, tg = lane & 3;
+constexpr float kLazy = 3.f;        // the reference M is raised when a score exceeds it by 2^3
+constexpr float kPScale = 5.f;      // p is held times 2^5: at most 2^8, below e4m3's 448
+
+// Columns of the B operands: head h, part i in column STR h + i; NH heads.
+template <int STR, int NH>
+struct Cols {
+  static constexpr int N = STR * NH;
+  static constexpr int QPARTS = STR == 4 ? 4 : 6;
+  static constexpr int PPARTS = STR == 4 ? 3 : 6;
+  static constexpr int TMEM = N <= 16 ? 64 : (N <= 32 ? 128 : 256);   // S(even), S(odd), O
+  static constexpr int CTAS = N <= 32 ? 2 : 1;                        // blocks an SM (shared memory)
+  static __host__ __device__ int smem(int m) {
+    return kStages * (kStageV + ((m + 31) & ~31) * TT) + 4 * N * TT + (int)sizeof(AttendMisc);
+  }
+};
+
+template <int STR, int NH>
+__global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_kernel(PagedView c, DecodeP p, int G) {
+  using CC = Cols<STR, NH>;
+  constexpr int N = CC::N;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  const int stage_bytes = kStageV + ((c.m + 31) & ~31) * TT;
+  const int off_q = kStages * stage_bytes, off_p = off_q + 2 * N * TT;
+  AttendMisc& ms = *reinterpret_cast<AttendMisc*>(dyn + off_p + 2 * N * TT);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const uint32_t smem0 = smem_u32(dyn);
 
   // ---- this block's share [t0, t1) of the flat tile sequence (the lengths were written before the
   // selection kernel started, which released this one after its own wait)
@@ -348,9 +441,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     __syncthreads();
-    if (lane == 0) scan[w] = x;
+    if (lane == 0) ms.scan[w] = x;
     __syncthreads();
-    for (int y = 0; y < kWarps; ++y) total += scan[y];
+    for (int y = 0; y < kThreads / 32; ++y) total += ms.scan[y];
   }
   total *= c.Hkv;
   const long long nb = min((long long)gridDim.x, total);      // every share has a tile
@@ -359,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     return;
   }
   const long long t0 = blockIdx.x * total / nb, t1 = (blockIdx.x + 1) * total / nb;
+  const int n_my = (int)(t1 - t0);
   // the unit that holds tile t0
   {
     long long before = 0;
@@ -373,319 +467,376 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
         if (lane >= o) sum += y;
       }
       __syncthreads();
-      if (lane == 31) scan[w] = sum;
+      if (lane == 31) ms.scan[w] = sum;
       __syncthreads();
       long long off = before, all = 0;
-      for (int y = 0; y < kWarps; ++y) {
-        if (y < w) off += scan[y];
-        all += scan[y];
+      for (int y = 0; y < kThreads / 32; ++y) {
+        if (y < w) off += ms.scan[y];
+        all += ms.scan[y];
       }
       const long long first = (off + sum - x) * c.Hkv, last = (off + sum) * c.Hkv;
       if (x > 0 && t0 >= first && t0 < last) {
         const int r = (int)(t0 - first);
-        s_cur.b = b;
-        s_cur.g = r / x;
-        s_cur.tile = r % x;
-        s_cur.u = b * c.Hkv + r / x;
-        s_cur.len = len;
+        ms.cur.b = b;
+        ms.cur.g = r / x;
+        ms.cur.tile = r % x;
+        ms.cur.u = b * c.Hkv + r / x;
+        ms.cur.len = len;
       }
       before += all;
     }
-    __syncthreads();
   }
+  // ---- barriers, tensor memory, the columns of p that no head or part uses (zeros for good)
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ms.full[i], kCopyThreads);
+      mbar_init(&ms.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], kSoftThreads);
+      mbar_init(&ms.pv_done[i], 1);
+    }
+    mbar_init(&ms.drain, 1);
+    fence_barrier_init();
+    ms.abort = 0;
+  }
+  if (w == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)),
+                 "r"((uint32_t)CC::TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  for (int i = tid; i < 2 * N * TT / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(dyn + off_p + 16 * i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  const Cursor start = ms.cur;
   pdl_wait();                               // the selection's results; the merge of an earlier call has read its parts
   pdl_launch_dependents();
-  if (tid == 0) {
+
+  if (w >= kCopyWarp0) {
+    // ================= copies =================
+    const int ct = tid - kCopyWarp0 * 32, lc = ct & 7, lr = ct >> 3;   // chunk and first row of every tile
+    const int pmask = (1 << c.page_log2) - 1;
+    Cursor cur = start;
+    int iu = -1, ord = -1, icount = 0, announced = 0;
+    uint2 rows = make_uint2(0, 0);
+    // page of 16 tokens of the cursor's tile, chunk `lane` (lanes 0..7 of every copy warp)
+    auto page_of_chunk = [&]() {
+      int pid = -1;
+      const int t = cur.tile * TT + 16 * lane;
+      if (lane < TT / 16 && t < cur.len) {
+        pid = __ldg(c.table + (size_t)cur.b * c.max_pages + (t >> c.page_log2));
+        if (pid < 0 || pid >= c.n_pages) {
+          pid = -1;
+          report_arg(c);
+        }
+      }
+      return pid;
+    };
+    // tiles up to `to` have landed: tell the product warp
+    auto announce = [&](int to) {
+      fence_proxy_async_smem();
+      for (; announced <= to; ++announced) mbar_arrive(&ms.full[announced % kStages]);
+    };
+    int mypid = page_of_chunk();
+    for (int t = 0; t < n_my; ++t) {
+      const int st = t % kStages;
+      if (t >= kStages) wait_or_abort(&ms.empty[st], ((t / kStages) - 1) & 1, &ms.abort, p.ctrl);
+      const uint32_t vbase = smem0 + st * stage_bytes, kbase = vbase + kStageV;
+      const int tb = cur.tile * TT;
+      // values: rows lr, lr + 16, ..., 16 dims each; rows past the length are zeros
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = lr + 16 * i;
+        const int pid = __shfl_sync(0xffffffffu, mypid, i);
+        const bool in = pid >= 0 && tb + r < cur.len;
+        const uint8_t* src = in ? c.v + c.vblock(pid, cur.g) + (size_t)((tb + r) & pmask) * D + lc * 16 : c.v;
+        cp_async16_zfill(vbase + r * D + ((lc ^ (r & 7)) << 4), src, in);
+      }
+      const int pid = __shfl_sync(0xffffffffu, mypid, lc);
+      if (ct < TT / 16) {                     // scales of the tile's pages; lc == ct here
+        if (pid >= 0) {
+          const size_t si = (size_t)pid * c.Hkv + cur.g;
+          cp_async_small<4>(&ms.ks[st][ct], c.ks + si);
+          cp_async_small<4>(&ms.vs[st][ct], c.vs + si);
+        } else {
+          ms.ks[st][ct] = -1.f;
+          ms.vs[st][ct] = 1.f;
+        }
+      }
+      if (cur.u != iu) {
+        iu = cur.u;
+        ++ord;
+        rows = *reinterpret_cast<const uint2*>(p.ulist + (size_t)iu * D + lr * 8);
+        icount = p.ucount[iu];
+        if (ord >= 2) {
+          // the buffer of unit ord - 2 is free once the products of tile t - 2 are done; they wait for tile
+          // t - 1 to be announced
+          cp_async_wait<0>();                 // committed copies: up to tile t - 1
+          announce(t - 1);
+          wait_or_abort(&ms.empty[(t - 2) % kStages], ((t - 2) / kStages) & 1, &ms.abort, p.ctrl);
+        }
+        const uint32_t qbase = smem0 + off_q + (ord & 1) * N * TT;
+        for (int i = ct; i < N * 8; i += kCopyThreads) {
+          const int r = i >> 3, ch = i & 7;
+          cp_async16_zfill(qbase + r * D + ((ch ^ (r & 7)) << 4), p.qpart + ((size_t)iu * N + r) * D + ch * 16, true);
+        }
+      }
+      // kept key rows lr, lr + 16, ..., chunk lc of 16 tokens; rows past the union up to the next
+      // multiple of 32 are zeros
+      const uint8_t* kb = c.k;
+      if (pid >= 0) kb += c.kblock(pid, cur.g) + ((tb + 16 * lc) & pmask);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = lr + 16 * i;
+        if (16 * i >= ((icount + 31) & ~31)) break;
+        const int d = (i < 4 ? rows.x >> (8 * i) : rows.y >> (8 * (i - 4))) & 0xff;
+        const bool in = pid >= 0 && r < icount;
+        cp_async16_zfill(kbase + r * TT + ((lc ^ (r & 7)) << 4), kb + (in ? (size_t)d << c.page_log2 : 0), in);
+      }
+      cp_async_commit();
+      if (t + 1 < n_my) {
+        next_tile(c, p, cur);
+        mypid = page_of_chunk();
+      }
+      if (t > 0 && announced < t) {
+        cp_async_wait<1>();
+        announce(t - 1);
+      }
+    }
+    cp_async_wait<0>();
+    announce(n_my - 1);
+  } else if (w == kMmaWarp) {
+    // ================= products =================
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(N);
+      Cursor cur = start;                     // tile whose scores are issued next
+      int iu = -1, ord = -1, nk = 0;
+      uint32_t firsts = 0;                    // bit t & 31: tile t is the first of its segment
+      bool ok = true;
+      auto issue_s = [&](int t) {
+        firsts &= ~(1u << (t & 31));
+        if (cur.u != iu) {
+          iu = cur.u;
+          ++ord;
+          nk = (p.ucount[iu] + 31) >> 5;
+          firsts |= 1u << (t & 31);
+        }
+        ok = wait_or_abort(&ms.full[t % kStages], (t / kStages) & 1, &ms.abort, p.ctrl);
+        if (!ok) return;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes + kStageV);
+        const uint64_t bd = smem_desc(smem0 + off_q + (ord & 1) * N * TT);
+        for (int k = 0; k < nk; ++k)          // 32 dims: 32 rows of A, 32 bytes of B's rows
+          tc_mma_f8(tmem + (t & 1) * N, ad + k * (32 * TT >> 4), bd + k * 2, idesc, k > 0);
+        tc_commit(&ms.s_full[t & 1]);
+        if (t + 1 < n_my) next_tile(c, p, cur);
+      };
+      issue_s(0);
+      for (int t = 0; ok && t < n_my; ++t) {
+        if (t + 1 < n_my) issue_s(t + 1);     // its buffer was read before p(t - 1) was announced
+        if (!ok || !(ok = wait_or_abort(&ms.p_full[t & 1], (t >> 1) & 1, &ms.abort, p.ctrl))) break;
+        tc_fence_after();
+        const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes);
+        const uint64_t bd = smem_desc(smem0 + off_p + (t & 1) * N * TT);
+        const bool first = (firsts >> (t & 31)) & 1u;
+#pragma unroll
+        for (int k = 0; k < TT / 32; ++k)
+          tc_mma_f8(tmem + 2 * N, ad + k * (32 * D >> 4), bd + k * 2, idesc, k > 0 || !first);
+        tc_commit(&ms.pv_done[t & 1]);
+        tc_commit(&ms.empty[t % kStages]);
+      }
+      tc_commit(&ms.drain);                   // nothing is in flight when tensor memory is given back
+      mbar_wait_bounded(&ms.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax: thread = token of the tile, and dim of the output =================
+    Cursor cur = start;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
+    float fac[NH], ref[NH], l[NH];
+    bool fresh = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      wait_or_abort(bar, parity, &ms.abort, p.ctrl);
+      __syncwarp();                           // what follows is executed by whole warps
+    };
+    int seg_start = 0, seg_tiles = 0;
+    // this thread's byte in row n of p: chunk (tid / 16) ^ (n % 8)
+    const uint32_t pcol = (uint32_t)(tid & 15);
+    const uint32_t pchunk = (uint32_t)(tid >> 4);
+    for (int t = 0; t < n_my; ++t) {
+      if (fresh) {
+        fresh = false;
+        seg_start = cur.tile;
+        seg_tiles = 0;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          fac[h] = h < G ? p.qfac[(size_t)cur.u * kMaxG + h] : 0.f;
+          ref[h] = -INFINITY;
+          l[h] = 0.f;
+        }
+      }
+      const int st = t % kStages, buf = t & 1;
+      wait(&ms.full[st], (t / kStages) & 1);  // the scales
+      wait(&ms.s_full[buf], (t >> 1) & 1);
+      tc_fence_after();
+      const float ksc = ms.ks[st][tid >> 4], vsc = ms.vs[st][tid >> 4];
+      const bool seen = ksc >= 0.f && cur.tile * TT + tid < cur.len;
+      const float lv = __log2f(vsc), iv = 1.f / vsc;
+      float x[NH];
+      bool raise = false;
+#pragma unroll
+      for (int cb = 0; cb < N; cb += 16) {
+        float v[16];
+        tmem_ld16(lane_base + buf * N + cb, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int hl = 0; hl < 16 / STR; ++hl) {
+          const int h = cb / STR + hl;
+          float s = v[hl * STR + CC::QPARTS - 1];
+#pragma unroll
+          for (int i = CC::QPARTS - 2; i >= 0; --i) s = fmaf(s, 1.f / 16.f, v[hl * STR + i]);
+          x[h] = seen ? fmaf(s, fac[h] * ksc, lv) : -INFINITY;
+          raise |= h < G && x[h] > ref[h] + kLazy;
+        }
+      }
+      if (named_bar_or(1, kSoftThreads, raise)) {
+        // a score far above the reference (always in a unit's first tile): raise it to the tile's maximum
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (h >= G) break;
+          float m = x[h];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) ms.red[w][h] = m;
+        }
+        named_bar_sync(1, kSoftThreads);
+        float al[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          al[h] = 1.f;
+          if (h >= G) continue;
+          const float m = fmaxf(fmaxf(ms.red[0][h], ms.red[1][h]), fmaxf(ms.red[2][h], ms.red[3][h]));
+          if (m > ref[h]) {
+            al[h] = fast_exp2(ref[h] - m);
+            ref[h] = m;
+            l[h] *= al[h];
+          }
+        }
+        if (seg_tiles > 0) {
+          wait(&ms.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int cb = 0; cb < N; cb += 16) {
+            float v[16];
+            tmem_ld16(lane_base + 2 * N + cb, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= al[(cb + i) / STR];
+            tmem_st16(lane_base + 2 * N + cb, v);
+          }
+          tmem_wait_st();
+        }
+        named_bar_sync(1, kSoftThreads);      // ms.red is free again
+      }
+      if (t >= 2) wait(&ms.pv_done[buf], ((t - 2) >> 1) & 1);
+      uint8_t* pb = dyn + off_p + buf * N * TT + pcol;
+#pragma unroll
+      for (int h = 0; h < NH; h += 2) {
+        if (h >= G) break;
+        float a0 = fast_exp2(x[h] - (ref[h] == -INFINITY ? 0.f : ref[h]) + kPScale);
+        float a1 = h + 1 < G ? fast_exp2(x[h + 1] - (ref[h + 1] == -INFINITY ? 0.f : ref[h + 1]) + kPScale) : 0.f;
+        l[h] = fmaf(a0, iv, l[h]);
+        l[h + 1] = fmaf(a1, iv, l[h + 1]);
+#pragma unroll
+        for (int i = 0; i < CC::PPARTS; ++i) {
+          const uint16_t code = f32x2_to_e4m3x2(a0, a1);
+          const int n0 = h * STR + i, n1 = n0 + STR;
+          pb[n0 * TT + ((pchunk ^ (n0 & 7)) << 4)] = (uint8_t)code;
+          pb[n1 * TT + ((pchunk ^ (n1 & 7)) << 4)] = (uint8_t)(code >> 8);
+          if (i + 1 < CC::PPARTS) {
+            const float2 back = e4m3x2_to_f32x2(code);
+            a0 = (a0 - back.x) * 16.f;
+            a1 = (a1 - back.y) * 16.f;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&ms.p_full[buf]);
+      ++seg_tiles;
+
+      // ---- end of the unit, or of this block's share of it
+      const bool last_tile = cur.tile + 1 == n_tiles(cur.len);
+      if (!last_tile && t + 1 < n_my) {
+        ++cur.tile;
+        continue;
+      }
+      const bool whole = seg_start == 0 && last_tile;
+      const size_t row0 = (size_t)cur.b * p.Hq + (size_t)cur.g * G;
+      const int slot = 2 * blockIdx.x + (t + 1 > seg_tiles ? 1 : 0);      // 0: the share's first piece
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if (h >= G) break;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (lane == 0) ms.red[w][h] = l[h];
+      }
+      named_bar_sync(1, kSoftThreads);
+      wait(&ms.pv_done[buf], (t >> 1) & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int cb = 0; cb < N; cb += 16) {
+        float v[16];
+        tmem_ld16(lane_base + 2 * N + cb, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int hl = 0; hl < 16 / STR; ++hl) {
+          const int h = cb / STR + hl;
+          if (h >= G) continue;
+          float O = v[hl * STR + CC::PPARTS - 1];
+#pragma unroll
+          for (int i = CC::PPARTS - 2; i >= 0; --i) O = fmaf(O, 1.f / 16.f, v[hl * STR + i]);
+          const float L = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
+          // p was held times 2^kPScale, so M + log2 l is off by it
+          const float M = ref[h] - kPScale;
+          if (whole) {
+            store_out_elem(p, (row0 + h) * D + tid, normalised(O, L));
+            if (p.lse_out && tid == 0) p.lse_out[row0 + h] = lse_of(M, L);
+          } else {
+            p.part_o[((size_t)slot * kMaxG + h) * D + tid] = O;
+            if (tid == 0) p.part_ml[(size_t)slot * kMaxG + h] = make_float2(M, L);
+          }
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(1, kSoftThreads);        // ms.red is free again
+      if (t + 1 < n_my) {
+        fresh = true;
+        next_unit(c, p, cur);
+      }
+    }
+  }
+  // the block's place among the units it shares with others, for the merge
+  if (tid == kMmaWarp * 32 + 1) {
     int4 sp = make_int4(-1, 0, 0, 0);
-    if (s_cur.tile > 0) {
+    if (start.tile > 0) {
       // the unit's tiles are [f, f + n) of the flat sequence; tile x lies in block ((x + 1) nb - 1) / total
-      const long long f = t0 - s_cur.tile, n = n_tiles(s_cur.len);
+      const long long f = t0 - start.tile, n = n_tiles(start.len);
       const long long first = ((f + 1) * nb - 1) / total, last = ((f + n) * nb - 1) / total;
-      sp = make_int4(s_cur.u, (int)first, (int)last, first * total / nb < f ? 1 : 0);
+      sp = make_int4(start.u, (int)first, (int)last, first * total / nb < f ? 1 : 0);
     }
     p.split[blockIdx.x] = sp;
   }
-
-  const int lc = tid & 7, lr = tid >> 3;    // this thread's chunk and first row of every copied tile
-  const uint32_t smem0 = smem_u32(dyn);
-  const int pmask = (1 << c.page_log2) - 1;
-
-  Cursor ic = s_cur;                        // next tile to issue
-  int iu = -1;                              // unit whose rows are in `rows`
-  uint2 rows = make_uint2(0, 0);
-  int icount = 0;
-  const int n_my = (int)(t1 - t0);
-  int issued = 0;
-
-  // page of 16 tokens of the tile at the issue cursor (threads 0..7, one chunk each)
-  auto page_of_chunk = [&]() {
-    int pid = -1;
-    const int t = ic.tile * TT + 16 * tid;
-    if (tid < TT / 16 && t < ic.len) {
-      pid = __ldg(c.table + (size_t)ic.b * c.max_pages + (t >> c.page_log2));
-      if (pid < 0 || pid >= c.n_pages) {
-        pid = -1;
-        report_arg(c);
-      }
-    }
-    return pid;
-  };
-  auto issue = [&]() {
-    TileMeta& md = meta[issued % kMeta];
-    if (ic.u != iu) {
-      iu = ic.u;
-      rows = *reinterpret_cast<const uint2*>(p.ulist + (size_t)iu * D + lr * 8);
-      icount = p.ucount[iu];
-    }
-    const uint32_t vbase = smem0 + (issued % kStages) * stage_bytes, kbase = vbase + kStageV;
-    const int tb = ic.tile * TT;
-    // values: rows lr, lr + 16, ..., chunk lc of 16 dims; rows past the length are zeros
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = lr + 16 * i, t = tb + r;
-      const int pid = md.pid[i];
-      const bool ok = pid >= 0 && t < ic.len;
-      const uint8_t* src = ok ? c.v + c.vblock(pid, ic.g) + (size_t)(t & pmask) * D + lc * 16 : c.v;
-      cp_async16_zfill(vbase + r * D + ((lc ^ (((r >> 3) & 3) * 2)) << 4), src, ok);
-    }
-    // kept key rows lr, lr + 16, ..., chunk lc of 16 tokens; rows past the union up to the next
-    // multiple of 16 are zeros
-    const int pid = md.pid[lc];
-    const uint8_t* kb = c.k;
-    if (pid >= 0) kb += c.kblock(pid, ic.g) + ((tb + 16 * lc) & pmask);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (16 * i >= icount) break;
-      const int r = lr + 16 * i;
-      const int d = (i < 4 ? rows.x >> (8 * i) : rows.y >> (8 * (i - 4))) & 0xff;
-      const bool ok = pid >= 0 && r < icount;
-      cp_async16_zfill(kbase + r * TT + ((lc ^ (((r >> 2) & 3) * 2)) << 4), kb + (ok ? (size_t)d << c.page_log2 : 0),
-                       ok);
-    }
-    // scales of the tile's pages
-    if (tid < TT / 16) {
-      if (pid >= 0) {                       // lc == tid here
-        const size_t si = (size_t)pid * c.Hkv + ic.g;
-        cp_async_small<4>(&md.ks[tid], c.ks + si);
-        cp_async_small<4>(&md.vs[tid], c.vs + si);
-      } else {
-        md.ks[tid] = -1.f;
-        md.vs[tid] = 1.f;
-      }
-    }
-    ++issued;
-    if (issued < n_my && ++ic.tile >= n_tiles(ic.len)) next_unit(c, p, ic);
-  };
-
-  if (tid < TT / 16) meta[0].pid[tid] = page_of_chunk();
   __syncthreads();
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (issued < n_my) issue();
-    cp_async_commit();
-    if (issued < n_my && tid < TT / 16) meta[issued % kMeta].pid[tid] = page_of_chunk();
-    __syncthreads();
-  }
-
-  // ---- consume
-  Cursor cc = s_cur;
-  uint2 qf[8][NT];
-  float fac[NT];
-  float o[NT][8][4];
-  float mx[NT], l[NT];
-  int nks = 0;
-  bool fresh = true;
-  const int seg_first = cc.tile;
-  int seg_start = seg_first;
-
-  for (int it = 0; it < n_my; ++it) {
-    const int st = it % kStages;
-    if (fresh) {
-      fresh = false;
-      nks = (p.ucount[cc.u] + 15) >> 4;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) qf[ks][nt] = p.qfrag[(((size_t)cc.u * 8 + ks) * NT + nt) * 32 + lane];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        fac[nt] = 4 * nt + tg < G ? p.qfac[(size_t)cc.u * kMaxG + 4 * nt + tg] : 0.f;
-        mx[nt] = -INFINITY;
-        l[nt] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-      }
-      seg_start = cc.tile;
-    }
-    cp_async_wait<kStages - 2>();
-    __syncthreads();
-    // refill the stage that was consumed in the previous iteration; the page ids of the tile after that
-    // are fetched now and stored once this tile is done
-    if (issued < n_my) issue();
-    cp_async_commit();
-    const int stage_next = issued < n_my ? issued % kMeta : -1;
-    int next_pid = -1;
-    if (stage_next >= 0) next_pid = page_of_chunk();
-    // ---- scores of this warp's 32 tokens: token 4 gr + j of the warp is row gr of product j / 2, low
-    // half for even j, high half (row gr + 8) for odd j
-    uint8_t* vt = dyn + st * stage_bytes;
-    const uint8_t* kt = vt + kStageV;
-    const int chunk = 2 * w + (gr >> 2);
-    const float ksc = meta[it % kMeta].ks[chunk], vsc = meta[it % kMeta].vs[chunk];
-    float s[NT][2][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][x][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      if (ks < nks) {
-        const uint8_t* kr = kt + (16 * ks + 4 * tg) * TT + ((chunk ^ (2 * tg)) << 4) + 4 * (gr & 3);
-        const uint32_t r0 = *reinterpret_cast<const uint32_t*>(kr);
-        const uint32_t r1 = *reinterpret_cast<const uint32_t*>(kr + TT);
-        const uint32_t r2 = *reinterpret_cast<const uint32_t*>(kr + 2 * TT);
-        const uint32_t r3 = *reinterpret_cast<const uint32_t*>(kr + 3 * TT);
-        const uint32_t a01 = __byte_perm(r0, r1, 0x5140), a23 = __byte_perm(r0, r1, 0x7362);
-        const uint32_t b01 = __byte_perm(r2, r3, 0x5140), b23 = __byte_perm(r2, r3, 0x7362);
-        const uint32_t A0[4] = {e4m3x2_to_f16x2((uint16_t)a01), e4m3x2_to_f16x2((uint16_t)(a01 >> 16)),
-                                e4m3x2_to_f16x2((uint16_t)b01), e4m3x2_to_f16x2((uint16_t)(b01 >> 16))};
-        const uint32_t A1[4] = {e4m3x2_to_f16x2((uint16_t)a23), e4m3x2_to_f16x2((uint16_t)(a23 >> 16)),
-                                e4m3x2_to_f16x2((uint16_t)b23), e4m3x2_to_f16x2((uint16_t)(b23 >> 16))};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(s[nt][0], A0, qf[ks][nt].x, qf[ks][nt].y);
-          mma_f16_16816(s[nt][1], A1, qf[ks][nt].x, qf[ks][nt].y);
-        }
-      }
-    }
-    // ---- running softmax; head 4 nt + tg, tokens 4 gr + {0, 1, 2, 3} of the warp
-    const int tok = cc.tile * TT + 32 * w + 4 * gr;
-    const bool page_ok = ksc >= 0.f;
-    const float lv = __log2f(vsc), iv = 1.f / vsc;
-    uint32_t pb[NT][2][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float f = fac[nt] * ksc;
-      float x[4];
-      x[0] = (s[nt][0][0] + s[nt][0][1]) * f + lv;
-      x[1] = (s[nt][0][2] + s[nt][0][3]) * f + lv;
-      x[2] = (s[nt][1][0] + s[nt][1][1]) * f + lv;
-      x[3] = (s[nt][1][2] + s[nt][1][3]) * f + lv;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!page_ok || tok + j >= cc.len) x[j] = -INFINITY;
-      float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float mn = fmaxf(mx[nt], m);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float al = fast_exp2(mx[nt] - ref);
-      mx[nt] = mn;
-      l[nt] *= al;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][i][e] *= al;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float pj = fast_exp2(x[j] - ref);
-        l[nt] = fmaf(pj, iv, l[nt]);
-        const float hi = __half2float(__float2half_rn(pj));
-        pb[nt][j >> 1][j & 1] = movmatrix_trans(pack_f16(hi, pj - hi));
-      }
-    }
-    // ---- O^T += V^T p^T: product x takes the tokens of score product x
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint8_t* vr = vt + (32 * w + 8 * tg + 2 * x) * D + ((gr ^ (2 * tg)) << 4);
-      const uint4 v0 = *reinterpret_cast<const uint4*>(vr);                 // token 8 tg + 2 x
-      const uint4 v2 = *reinterpret_cast<const uint4*>(vr + D);             // + 1: rows 8.. of the k index
-      const uint4 v1 = *reinterpret_cast<const uint4*>(vr + 4 * D);         // + 4: the odd k index
-      const uint4 v3 = *reinterpret_cast<const uint4*>(vr + 5 * D);
-      const uint32_t* p0 = reinterpret_cast<const uint32_t*>(&v0);
-      const uint32_t* p1 = reinterpret_cast<const uint32_t*>(&v1);
-      const uint32_t* p2 = reinterpret_cast<const uint32_t*>(&v2);
-      const uint32_t* p3 = reinterpret_cast<const uint32_t*>(&v3);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t a01 = __byte_perm(p0[q], p1[q], 0x5140), a23 = __byte_perm(p0[q], p1[q], 0x7362);
-        const uint32_t b01 = __byte_perm(p2[q], p3[q], 0x5140), b23 = __byte_perm(p2[q], p3[q], 0x7362);
-        const uint32_t A0[4] = {e4m3x2_to_f16x2((uint16_t)a01), e4m3x2_to_f16x2((uint16_t)(a01 >> 16)),
-                                e4m3x2_to_f16x2((uint16_t)b01), e4m3x2_to_f16x2((uint16_t)(b01 >> 16))};
-        const uint32_t A1[4] = {e4m3x2_to_f16x2((uint16_t)a23), e4m3x2_to_f16x2((uint16_t)(a23 >> 16)),
-                                e4m3x2_to_f16x2((uint16_t)b23), e4m3x2_to_f16x2((uint16_t)(b23 >> 16))};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(o[nt][2 * q], A0, pb[nt][x][0], pb[nt][x][1]);
-          mma_f16_16816(o[nt][2 * q + 1], A1, pb[nt][x][0], pb[nt][x][1]);
-        }
-      }
-    }
-    if (stage_next >= 0 && tid < TT / 16) meta[stage_next].pid[tid] = next_pid;
-
-    // ---- end of the unit, or of this block's share of it
-    const bool last_tile = cc.tile + 1 == n_tiles(cc.len);
-    if (!last_tile && it + 1 < n_my) {
-      ++cc.tile;
-      continue;
-    }
-    // merge the four warps (in this tile's value buffer, which is refilled only after the next
-    // iteration's barrier): O column pairs, rows d = 16 gr + 2 i (+ 1)
-    static_assert(kWarps * kMaxG * D * 4 <= kStageV, "merge buffer");
-    float* merge_o = reinterpret_cast<float*>(vt);          // [kWarps][G][D]
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float lt = l[nt];
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, d);
-      const int hh = 4 * nt + tg;
-      if (hh < G) {
-        if (gr == 0) {
-          merge_ml[w][hh][0] = mx[nt];
-          merge_ml[w][hh][1] = lt;
-        }
-        float* mo = merge_o + ((size_t)w * G + hh) * D + 16 * gr;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float2*>(mo + 2 * i) =
-              make_float2(o[nt][i][0] + o[nt][i][1], o[nt][i][2] + o[nt][i][3]);
-      }
-    }
-    __syncthreads();
-    const bool whole = seg_start == 0 && last_tile;
-    const size_t row0 = (size_t)cc.b * p.Hq + (size_t)cc.g * G;
-    const int slot = 2 * blockIdx.x + (it + 1 - (cc.tile + 1 - seg_start) > 0 ? 1 : 0);   // 0: the share's first piece
-    for (int hh = 0; hh < G; ++hh) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) M = fmaxf(M, merge_ml[x][hh][0]);
-      const float ref = M == -INFINITY ? 0.f : M;
-      float L = 0.f, O = 0.f;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        const float f = fast_exp2(merge_ml[x][hh][0] - ref);
-        L = fmaf(merge_ml[x][hh][1], f, L);
-        O = fmaf(merge_o[((size_t)x * G + hh) * D + tid], f, O);
-      }
-      if (whole) {
-        store_out_elem(p, (row0 + hh) * D + tid, normalised(O, L));
-        if (p.lse_out && tid == 0) p.lse_out[row0 + hh] = lse_of(M, L);
-      } else {
-        p.part_o[((size_t)slot * kMaxG + hh) * D + tid] = O;
-        if (tid == 0) p.part_ml[(size_t)slot * kMaxG + hh] = make_float2(M, L);
-      }
-    }
-    __syncthreads();                        // the merge buffers are free again
-    if (it + 1 < n_my) {
-      fresh = true;
-      next_unit(c, p, cc);
-    }
-  }
-  cp_async_wait<0>();
+  if (w == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)CC::TMEM) : "memory");
 }
 
 // ============================================================================
@@ -753,11 +904,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView
 
 // ---------------------------------------------------------------- host side
 struct Layout {
-  size_t ucount, ulist, qfrag, qfac, part_ml, part_o, split, total;
+  size_t ucount, ulist, qpart, qfac, part_ml, part_o, split, total;
 };
 
+// The workspace does not depend on the output type: room for the widest operands.
 Layout layout_of(int n_units, int G, int blocks) {
-  const int NT = G > 4 ? 2 : 1;
+  const int cols = G > 4 ? 64 : 32;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t r = at;
@@ -767,7 +919,7 @@ Layout layout_of(int n_units, int G, int blocks) {
   Layout y;
   y.ucount = take((size_t)n_units * 4);
   y.ulist = take((size_t)n_units * D);
-  y.qfrag = take((size_t)n_units * 8 * NT * 32 * sizeof(uint2));
+  y.qpart = take((size_t)n_units * cols * D);
   y.qfac = take((size_t)n_units * kMaxG * 4);
   y.part_ml = take((size_t)2 * blocks * kMaxG * sizeof(float2));
   y.part_o = take((size_t)2 * blocks * kMaxG * D * 4);
@@ -776,59 +928,61 @@ Layout layout_of(int n_units, int G, int blocks) {
   return y;
 }
 
-int attend_blocks() {
-  const int n = kCtasPerSm * device_sm_count();
+int attend_blocks(int per_sm) {
+  const int n = per_sm * device_sm_count();
   return n < kMaxParts ? n : kMaxParts;
 }
 
 template <typename T>
-cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NT, cudaStream_t st) {
+cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
   const dim3 grid(c.B * c.Hkv), block(kSelThreads);
-  if (G == 1) return launch_pdl(paged_select_kernel<T, 1>, grid, block, 0, st, c, p, G, NT);
-  if (G == 2) return launch_pdl(paged_select_kernel<T, 2>, grid, block, 0, st, c, p, G, NT);
-  if (G <= 4) return launch_pdl(paged_select_kernel<T, 4>, grid, block, 0, st, c, p, G, NT);
-  return launch_pdl(paged_select_kernel<T, 8>, grid, block, 0, st, c, p, G, NT);
+  if (G == 1) return launch_pdl(paged_select_kernel<T, 1>, grid, block, 0, st, c, p, G, NH, stride, parts);
+  if (G == 2) return launch_pdl(paged_select_kernel<T, 2>, grid, block, 0, st, c, p, G, NH, stride, parts);
+  if (G <= 4) return launch_pdl(paged_select_kernel<T, 4>, grid, block, 0, st, c, p, G, NH, stride, parts);
+  return launch_pdl(paged_select_kernel<T, 8>, grid, block, 0, st, c, p, G, NH, stride, parts);
 }
 
-template <int NT>
-int launch_attend(const PagedView& c, const DecodeP& p, int G, int blocks, cudaStream_t st) {
-  const int smem = kStages * (kStageV + ((c.m + 15) & ~15) * TT);
-  const int rc = set_smem_limit(paged_attend_kernel<NT>, smem, "paged_attend_kernel");
+template <int STR, int NH>
+int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStream_t st) {
+  using CC = Cols<STR, NH>;
+  const int smem = CC::smem(c.m), blocks = attend_blocks(CC::CTAS);
+  int rc = set_smem_limit(paged_attend_kernel<STR, NH>, smem, "paged_attend_kernel");
   if (rc != AQUA_OK) return rc;
-  const cudaError_t e = launch_pdl(paged_attend_kernel<NT>, dim3(blocks), dim3(kThreads), smem, st, c, p, G);
+  cudaError_t e = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NH, STR, CC::QPARTS, st)
+                       : launch_select<float>(c, p, G, NH, STR, CC::QPARTS, st);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
+  if ((rc = check_launch("paged_select_kernel")) != AQUA_OK) return rc;
+  e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
-  return check_launch("paged_attend_kernel");
+  if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK || blocks < 2) return rc;
+  e = launch_pdl(paged_merge_kernel, dim3(blocks - 1, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
+  return check_launch("paged_merge_kernel");
 }
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int n_units, int G) { return layout_of(n_units, G, attend_blocks()).total; }
+size_t paged_decode_workspace_bytes(int n_units, int G) { return layout_of(n_units, G, attend_blocks(2)).total; }
 
 int launch_paged_decode(const PagedView& c, const int32_t* len, const void* q, bool bf16, const Strides& qs,
                         const float* P, const RopeView& rope, int Hq, int k, float scale, void* out, bool out_bf16,
                         int32_t* sel_out, float* qproj_out, float* lse_out, void* ws, cudaStream_t st) {
-  const int n_units = c.B * c.Hkv, G = Hq / c.Hkv, NT = G > 4 ? 2 : 1, blocks = attend_blocks();
-  const Layout y = layout_of(n_units, G, blocks);
+  const int n_units = c.B * c.Hkv, G = Hq / c.Hkv;
+  const Layout y = layout_of(n_units, G, attend_blocks(2));
   uint8_t* base = static_cast<uint8_t*>(ws);
   DecodeP p;
   p.len = len; p.q = q; p.qs = qs; p.P = P; p.rope = rope; p.Hq = Hq; p.k = k; p.scale = scale;
   p.out = out; p.out_bf16 = out_bf16; p.sel_out = sel_out; p.qproj_out = qproj_out; p.lse_out = lse_out;
+  p.ctrl = c.ctrl;
   p.ucount = reinterpret_cast<int32_t*>(base + y.ucount);
   p.ulist = base + y.ulist;
-  p.qfrag = reinterpret_cast<uint2*>(base + y.qfrag);
+  p.qpart = base + y.qpart;
   p.qfac = reinterpret_cast<float*>(base + y.qfac);
   p.part_ml = reinterpret_cast<float2*>(base + y.part_ml);
-  p.split = reinterpret_cast<int4*>(base + y.split);
   p.part_o = reinterpret_cast<float*>(base + y.part_o);
-  cudaError_t e = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NT, st) : launch_select<float>(c, p, G, NT, st);
-  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
-  int rc = check_launch("paged_select_kernel");
-  if (rc != AQUA_OK) return rc;
-  rc = NT == 1 ? launch_attend<1>(c, p, G, blocks, st) : launch_attend<2>(c, p, G, blocks, st);
-  if (rc != AQUA_OK || blocks < 2) return rc;
-  e = launch_pdl(paged_merge_kernel, dim3(blocks - 1, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
-  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
-  return check_launch("paged_merge_kernel");
+  p.split = reinterpret_cast<int4*>(base + y.split);
+  if (out_bf16) return G > 4 ? launch_step<4, 8>(c, p, G, bf16, st) : launch_step<4, 4>(c, p, G, bf16, st);
+  return G > 4 ? launch_step<8, 8>(c, p, G, bf16, st) : launch_step<8, 4>(c, p, G, bf16, st);
 }
 
 }  // namespace aqua
