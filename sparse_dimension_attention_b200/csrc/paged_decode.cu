@@ -51,8 +51,7 @@ constexpr int kSoftThreads = 128;         // one thread per token of a tile
 constexpr int kMmaWarp = 4, kCopyWarp0 = 5;
 constexpr int kCopyThreads = 128;
 constexpr int kThreads = (kCopyWarp0 + kCopyThreads / 32) * 32;
-constexpr int kStages = 3;                // the copies of a tile are announced after those of the next are issued, and
-                                          // S(t + 1) is issued before O(t): two stages would wait on each other
+constexpr int kStages = 3;
 constexpr int kMaxG = 8;
 constexpr int kSelThreads = 512;
 
@@ -389,6 +388,28 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   }
 }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// For a polling loop that began at time `since` (0: sets it): whether to give up.
+__device__ __forceinline__ bool poll_abort(volatile int* abort, unsigned long long& since, int32_t* ctrl) {
+  const unsigned long long now = globaltimer_ns();
+  if (since == 0) since = now;
+  if (*abort) return true;
+  if (now - since <= kWaitLimitNs) return false;
+  *abort = 1;
+  record_status(ctrl, AQUA_ERR_TIMEOUT);
+  return true;
+}
+
 // Next unit with tokens after cur (its tiles are used up).
 __device__ __forceinline__ void next_unit(const PagedView& c, const DecodeP& p, Cursor& cur) {
   cur.tile = 0;
@@ -627,8 +648,6 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           nk = (p.ucount[iu] + 31) >> 5;
           firsts |= 1u << (t & 31);
         }
-        ok = wait_or_abort(&ms.full[t % kStages], (t / kStages) & 1, &ms.abort, p.ctrl);
-        if (!ok) return;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes + kStageV);
@@ -638,10 +657,21 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         tc_commit(&ms.s_full[t & 1]);
         if (t + 1 < n_my) next_tile(c, p, cur);
       };
-      issue_s(0);
-      for (int t = 0; ok && t < n_my; ++t) {
-        if (t + 1 < n_my) issue_s(t + 1);     // its buffer was read before p(t - 1) was announced
-        if (!ok || !(ok = wait_or_abort(&ms.p_full[t & 1], (t >> 1) & 1, &ms.abort, p.ctrl))) break;
+      // Whatever is ready first: the scores of tile t + 1 (its copies landed; its buffer was read before p(t - 1)
+      // was announced) or the values of tile t (p written).  In a fixed order either one would hold up the other.
+      int scored = 0;                         // tiles whose scores are issued
+      for (int t = 0; t < n_my; ++t) {
+        unsigned long long since = 0;
+        while (true) {
+          if (scored < n_my && scored <= t + 1 && mbar_test(&ms.full[scored % kStages], (scored / kStages) & 1))
+            issue_s(scored++);
+          if (scored > t && mbar_test(&ms.p_full[t & 1], (t >> 1) & 1)) break;
+          if (poll_abort(&ms.abort, since, p.ctrl)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes);
         const uint64_t bd = smem_desc(smem0 + off_p + (t & 1) * N * TT);
