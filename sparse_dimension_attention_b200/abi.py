@@ -241,18 +241,31 @@ def aqua_h2o_update(cache: aqua_cache, scores, lse, Hq: int, budget: int, recent
 
 # ------------------------------------------------------------------ paged 8-bit cache
 
+# These wrappers run once per layer and token, so they are kept to a few microseconds: types compared by
+# identity, the raw stream handle instead of a stream object.
+
+def _torch():
+    """torch, bound to this module at the first paged call (the module itself imports without it)."""
+    global torch, _IO
+    import torch
+    _IO = {torch.bfloat16: AQUA_BF16, torch.float32: AQUA_F32}
+    return torch
+
+
+torch = None
+_IO: dict = {}
+
+
 def _io_dtype(t, what: str) -> int:
-    name = str(t.dtype)
-    if name == "torch.bfloat16":
-        return AQUA_BF16
-    if name == "torch.float32":
-        return AQUA_F32
-    raise AquaError(AQUA_ERR_UNSUPPORTED, f"{what} must be bfloat16 or float32, not {name}")
+    io = (_IO or (_torch() and _IO)).get(t.dtype)
+    if io is None:
+        raise AquaError(AQUA_ERR_UNSUPPORTED, f"{what} must be bfloat16 or float32, not {t.dtype}")
+    return io
 
 
-def _want(t, shape, dtype: str, what: str) -> None:
+def _want(t, shape, dtype, what: str) -> None:
     """A dense device tensor of this shape and type, or AquaError: the C side sees addresses only."""
-    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise AquaError(AQUA_ERR_ARG, f"{what} must be a contiguous {dtype} device tensor of shape {tuple(shape)}, "
                                       f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -267,24 +280,25 @@ def _rows(t, heads: int, what: str) -> tuple[int, int]:
     return (row if t.shape[0] > 1 else 0), (head if heads > 1 else 0)
 
 
-class _on:
-    """Makes the device of `t` current for a call (streams and launches belong to a device)."""
+def _one_device(t, *others) -> int:
+    """Index of the one device all tensors of a call are on."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise AquaError(AQUA_ERR_ARG, f"tensors on device {o.get_device()} and {dev} in one call")
+    return dev
 
-    def __init__(self, t, *others):
-        import torch
-        self.dev = t.device
-        for o in others:
-            if o is not None and o.device != self.dev:
-                raise AquaError(AQUA_ERR_ARG, f"tensors on {o.device} and {self.dev} in one call")
-        self.ctx = torch.cuda.device(self.dev) if torch.cuda.current_device() != self.dev.index else None
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _call(fn, dev: int, stream, *args) -> None:
+    """fn(*args, stream) with `dev` current (launches and default streams belong to a device)."""
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc != AQUA_OK:
+        _check(rc)
 
 
 def _rope(rope):
@@ -299,20 +313,21 @@ def aqua_paged_status(cache: aqua_paged_cache, stream=None) -> int:
 
 def aqua_paged_append(cache: aqua_paged_cache, k_new, v_new, start, P, cu_new=None, rope=None, stream=None) -> None:
     """Rotate, project, quantise and append new tokens: k_new, v_new [n_tokens, Hkv, d] (bf16 or f32; tokens and
-    heads may be strided), start [B] int32, cu_new [B + 1] int32 or None for one token of each sequence, rope an AquaRope."""
+    heads may be strided), start [B] int32, cu_new [B + 1] int32 or None for one token of each sequence, rope an
+    AquaRope."""
+    io = _io_dtype(k_new, "k_new")
     ks, kh = _rows(k_new, cache.Hkv, "k_new")
     vs, vh = _rows(v_new, cache.Hkv, "v_new")
-    io = _io_dtype(k_new, "k_new")
-    if v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
+    if v_new.dtype is not k_new.dtype or v_new.shape != k_new.shape:
         raise AquaError(AQUA_ERR_ARG, "k_new and v_new must have the same type and shape")
-    _want(start, (cache.B,), "torch.int32", "start")
-    _want(P, (cache.Hkv, cache.d, cache.d), "torch.float32", "P")
+    _want(start, (cache.B,), torch.int32, "start")
+    _want(P, (cache.Hkv, cache.d, cache.d), torch.float32, "P")
     if cu_new is not None:
-        _want(cu_new, (cache.B + 1,), "torch.int32", "cu_new")
-    with _on(k_new, v_new, start, P, cu_new, rope):
-        _check(load_library().aqua_paged_append(
-            ctypes.byref(cache), _ptr(k_new), _ptr(v_new), io, ks, kh, vs, vh, k_new.shape[0], _ptr(start),
-            _ptr(cu_new), _ptr(P), _rope(rope), _stream(stream)))
+        _want(cu_new, (cache.B + 1,), torch.int32, "cu_new")
+    _call((_lib or load_library()).aqua_paged_append,
+          _one_device(k_new, v_new, start, P, cu_new, rope and rope.cos_sin), stream, ctypes.byref(cache),
+          k_new.data_ptr(), v_new.data_ptr(), io, ks, kh, vs, vh, k_new.shape[0], start.data_ptr(), _ptr(cu_new),
+          P.data_ptr(), _rope(rope))
 
 
 def aqua_paged_decode_workspace_size(cache: aqua_paged_cache, Hq: int) -> int:
@@ -321,33 +336,38 @@ def aqua_paged_decode_workspace_size(cache: aqua_paged_cache, Hq: int) -> int:
 
 def aqua_paged_decode_attn(cache: aqua_paged_cache, q, len, P, Hq: int, k: int, out, workspace, rope=None,
                            scale: float = 0.0, sel_out=None, qproj_out=None, lse_out=None, stream=None) -> None:
-    """One decode step over the pages: q [B, Hq, d] (rows and heads may be strided) at position len[b] - 1 of each sequence."""
-    qs, qh = _rows(q, Hq, "q")
+    """One decode step over the pages: q [B, Hq, d] (rows and heads may be strided) at position len[b] - 1 of each
+    sequence."""
     io = _io_dtype(q, "q")
-    if q.shape[0] != cache.B:
-        raise AquaError(AQUA_ERR_ARG, f"q has {q.shape[0]} rows for {cache.B} sequences")
     od = _io_dtype(out, "out")
-    _want(out, (cache.B, Hq, cache.d), str(out.dtype), "out")
-    _want(len, (cache.B,), "torch.int32", "len")
-    _want(P, (cache.Hkv, cache.d, cache.d), "torch.float32", "P")
+    qs, qh = _rows(q, Hq, "q")
+    B, d = cache.B, cache.d
+    if q.shape[0] != B:
+        raise AquaError(AQUA_ERR_ARG, f"q has {q.shape[0]} rows for {B} sequences")
+    _want(out, (B, Hq, d), out.dtype, "out")
+    _want(len, (B,), torch.int32, "len")
+    _want(P, (cache.Hkv, d, d), torch.float32, "P")
     if sel_out is not None:
-        _want(sel_out, (cache.B, Hq, k), "torch.int32", "sel_out")
+        _want(sel_out, (B, Hq, k), torch.int32, "sel_out")
     if qproj_out is not None:
-        _want(qproj_out, (cache.B, Hq, cache.d), "torch.float32", "qproj_out")
+        _want(qproj_out, (B, Hq, d), torch.float32, "qproj_out")
     if lse_out is not None:
-        _want(lse_out, (cache.B, Hq), "torch.float32", "lse_out")
-    with _on(q, len, P, out, workspace, rope):
-        _check(load_library().aqua_paged_decode_attn(
-            ctypes.byref(cache), _ptr(len), _ptr(q), io, qs, qh, _ptr(P), _rope(rope), Hq, k, scale, _ptr(out),
-            od, _ptr(sel_out), _ptr(qproj_out), _ptr(lse_out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream)))
+        _want(lse_out, (B, Hq), torch.float32, "lse_out")
+    if not workspace.is_contiguous():
+        raise AquaError(AQUA_ERR_ARG, "workspace must be contiguous")
+    _call((_lib or load_library()).aqua_paged_decode_attn,
+          _one_device(q, len, P, out, workspace, sel_out, qproj_out, lse_out, rope and rope.cos_sin), stream,
+          ctypes.byref(cache), len.data_ptr(), q.data_ptr(), io, qs, qh, P.data_ptr(), _rope(rope), Hq, k, scale,
+          out.data_ptr(), od, _ptr(sel_out), _ptr(qproj_out), _ptr(lse_out), workspace.data_ptr(),
+          workspace.nbytes)
 
 
 def aqua_paged_gather(cache: aqua_paged_cache, len, dst: aqua_cache, max_len: int, seq_idx=None, stream=None) -> None:
     """Copy sequences out of the pages into a contiguous cache (dst.max_len becomes max_len)."""
-    _want(len, (cache.B,), "torch.int32", "len")
+    if torch is None:
+        _torch()
+    _want(len, (cache.B,), torch.int32, "len")
     if seq_idx is not None:
-        _want(seq_idx, (dst.B,), "torch.int32", "seq_idx")
-    with _on(len, seq_idx):
-        _check(load_library().aqua_paged_gather(ctypes.byref(cache), _ptr(len), _ptr(seq_idx), ctypes.byref(dst),
-                                                max_len, _stream(stream)))
+        _want(seq_idx, (dst.B,), torch.int32, "seq_idx")
+    _call((_lib or load_library()).aqua_paged_gather, _one_device(len, seq_idx), stream, ctypes.byref(cache),
+          len.data_ptr(), _ptr(seq_idx), ctypes.byref(dst), max_len)

@@ -62,7 +62,7 @@ class AquaRope:
     def __init__(self, cos_sin: torch.Tensor, interleaved: bool = False):
         if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
             raise abi.AquaError(abi.AQUA_ERR_ARG, "cos_sin must be a contiguous f32 tensor [n_pos, rot_dim]")
-        self.cos_sin, self.device = cos_sin, cos_sin.device
+        self.cos_sin = cos_sin
         self.desc = abi.aqua_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)))
 
     @classmethod
