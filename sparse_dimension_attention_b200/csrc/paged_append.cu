@@ -276,6 +276,133 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
   }
 }
 
+// One new token for each sequence: a block takes up to kStepGroup sequences of one
+// KV head.  Bound by latency: P (64 KB, from L2) is read once per block into
+// registers before the wait on the previous kernel, and kept there as f64, whose
+// 64 multiply-adds a cycle and SM are enough here; the sums are then exact to f32
+// rounding, so that a code differs from the exact one only on a tie.  Warp t
+// writes token t.
+constexpr int kStepThreads = 512;
+constexpr int kStepGroup = 16;
+constexpr int kStepSlices = kStepThreads / D;              // slices of 32 input dims
+
+template <typename T>
+__global__ void __launch_bounds__(kStepThreads) paged_append_step_kernel(PagedView c, AppendParams a, int group) {
+  extern __shared__ __align__(16) double part[];           // [kStepSlices][group][D]
+  __shared__ __align__(16) double xs[kStepGroup][D];       // rotated rows
+  __shared__ float raw[kStepGroup][D];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
+  const int col = tid & (D - 1), sl = tid >> 7;
+  constexpr int R = D / kStepSlices;
+  float pf[R];
+  {
+    const float* Pg = a.P + ((size_t)h * D + sl * R) * D + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i) pf[i] = __ldg(Pg + (size_t)i * D);
+  }
+  pdl_wait();
+  const int b = blockIdx.x * group + w, nt = min(group, c.B - (int)blockIdx.x * group);
+  int pid = -1, slot = 0;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (w < nt) {
+    int token, n;
+    bool bad;
+    n = run_length(a, c, b, token, slot, bad);
+    if (n > 0) {
+      pid = __ldg(c.table + (size_t)b * c.max_pages + (slot >> c.page_log2));
+      if (pid < 0 || pid >= c.n_pages) {
+        pid = -1;
+        bad = true;
+      }
+    }
+    if (bad && lane == 0) report_arg(c);
+    if (pid >= 0) {
+      float f[4];
+      load4<T>(static_cast<const T*>(a.k_new) + (size_t)token * a.ks.row + (size_t)h * a.ks.head + 4 * lane, f);
+      load4<T>(static_cast<const T*>(a.v_new) + (size_t)token * a.vs.row + (size_t)h * a.vs.head + 4 * lane, v);
+      *reinterpret_cast<float4*>(&raw[w][4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+      __syncwarp();
+      const float* cs = a.rope.cs + (size_t)slot * a.rope.rot;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        xs[w][4 * lane + e] =
+            a.rope.cs != nullptr ? rotated<double>(raw[w], 4 * lane + e, cs, a.rope.rot, a.rope.interleaved) : (double)f[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xs[w][4 * lane + e] = 0.0;
+    }
+  }
+  double p[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) p[i] = pf[i];
+  __syncthreads();
+  for (int t = 0; t < nt; ++t) {
+    double s0 = 0.0, s1 = 0.0;
+#pragma unroll
+    for (int i = 0; i < R; i += 2) {
+      const double2 x = *reinterpret_cast<const double2*>(&xs[t][sl * R + i]);
+      s0 = fma(x.x, p[i], s0);
+      s1 = fma(x.y, p[i + 1], s1);
+    }
+    part[(sl * group + t) * D + col] = s0 + s1;
+  }
+  __syncthreads();
+  if (pid < 0) return;
+  float y[4];
+  float kmax = 0.f, vmax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double* q = part + w * D + lane + 32 * e;        // lane's dims: lane + 32 e
+    double sum = q[0];
+#pragma unroll
+    for (int x = 1; x < kStepSlices; ++x) sum += q[(size_t)x * group * D];
+    y[e] = (float)sum;
+    if (lane + 32 * e < c.m) kmax = fmaxf(kmax, finite_abs(y[e]));
+    vmax = fmaxf(vmax, finite_abs(v[e]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
+    vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+  }
+  const int fill = slot & ((1 << c.page_log2) - 1);
+  const size_t si = (size_t)pid * c.Hkv + h;
+  const float kold = fill > 0 ? c.ks[si] : 0.f, vold = fill > 0 ? c.vs[si] : 0.f;
+  const float ks = page_scale(kmax, kold, fill), vs = page_scale(vmax, vold, fill);
+  uint8_t* kb = c.k + c.kblock(pid, h);
+  uint8_t* vb = c.v + c.vblock(pid, h);
+  if (fill > 0 && ks != kold) recode_keys(kb, c.m, c.page_log2, fill, kold / ks, lane, 32);
+  if (fill > 0 && vs != vold) recode_values(vb, fill, vold / vs, lane, 32);
+  __syncwarp();                            // a 16-byte piece re-coded by one lane holds another lane's new byte
+  if (lane == 0) {
+    c.ks[si] = ks;
+    c.vs[si] = vs;
+  }
+  const float ki = 1.f / ks, vi = 1.f / vs;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int j = lane + 32 * e;
+    if (j < c.m) kb[((size_t)j << c.page_log2) + fill] = (uint8_t)f32x2_to_e4m3x2(y[e] * ki, 0.f);
+  }
+  reinterpret_cast<uint32_t*>(vb + (size_t)fill * D)[lane] =
+      f32x4_to_e4m3x4(v[0] * vi, v[1] * vi, v[2] * vi, v[3] * vi);
+}
+
+template <typename T>
+int launch_step(const PagedView& c, const AppendParams& a, cudaStream_t st) {
+  // enough sequences a block that the blocks fit the SMs at once
+  const int want = (c.B * c.Hkv + device_sm_count() - 1) / device_sm_count();
+  const int group = want < kStepGroup ? want : kStepGroup;
+  const int smem = kStepSlices * group * D * (int)sizeof(double);
+  const int rc = set_smem_limit(paged_append_step_kernel<T>, kStepSlices * kStepGroup * D * (int)sizeof(double),
+                                "paged_append_step_kernel");
+  if (rc != AQUA_OK) return rc;
+  const cudaError_t e = launch_pdl(paged_append_step_kernel<T>, dim3((c.B + group - 1) / group, c.Hkv),
+                                   dim3(kStepThreads), smem, st, c, a, group);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_append_step_kernel: %s", cudaGetErrorString(e));
+  return check_launch("paged_append_step_kernel");
+}
+
 template <typename T>
 int launch_run(const PagedView& c, const AppendParams& a, cudaStream_t st) {
   const int smem = ((D << c.page_log2) + kWarps * kGroup * D + 2 * kGroup * D) * (int)sizeof(float);
@@ -296,6 +423,7 @@ int launch_paged_append(const PagedView& c, const void* k_new, const void* v_new
   AppendParams a;
   a.k_new = k_new; a.v_new = v_new; a.ks = ks; a.vs = vs; a.start = start; a.cu = cu;
   a.P = P; a.rope = rope; a.n_tokens = n_tokens;
+  if (cu == nullptr) return bf16 ? launch_step<__nv_bfloat16>(c, a, st) : launch_step<float>(c, a, st);
   return bf16 ? launch_run<__nv_bfloat16>(c, a, st) : launch_run<float>(c, a, st);
 }
 

@@ -140,18 +140,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   __syncthreads();
   for (int i = tid; i < GP * D; i += kSelThreads) {
     const int hh = i >> 7;
-    double x = raw[hh][j];
-    if (p.rope.cs != nullptr && n > 0) {
-      const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
-      const int rot = p.rope.rot, half = rot >> 1;
-      if (j < rot) {
-        const bool first = p.rope.interleaved ? (j & 1) == 0 : j < half;
-        const int a = p.rope.interleaved ? j >> 1 : (first ? j : j - half);
-        const int o = p.rope.interleaved ? j ^ 1 : (first ? j + half : j - half);
-        const double cc = __ldg(cs + a), ss = __ldg(cs + half + a), y = raw[hh][o];
-        x = first ? x * cc - y * ss : x * cc + y * ss;
-      }
-    }
+    const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
+    const double x = p.rope.cs != nullptr && n > 0 ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved)
+                                                   : (double)raw[hh][j];
     qd[hh][j] = x;
   }
   __syncthreads();

@@ -90,9 +90,10 @@ __device__ __forceinline__ float pow2_scale(float amax) {
 
 // Element i of a row rotated to its position; row: the raw 128 elements (shared
 // memory), cs: the position's rot / 2 cosines, then its sines.
+// F: the type it is computed in.
 template <typename F>
-__device__ __forceinline__ F rotated(const F* row, int i, const float* cs, int rot, bool interleaved) {
-  const F x = row[i];
+__device__ __forceinline__ F rotated(const float* row, int i, const float* cs, int rot, bool interleaved) {
+  const F x = (F)row[i];
   if (i >= rot) return x;
   const int half = rot >> 1;
   int j, o;       // angle index, partner
@@ -107,7 +108,7 @@ __device__ __forceinline__ F rotated(const F* row, int i, const float* cs, int r
     o = first ? i + half : i - half;
   }
   const F c = (F)__ldg(cs + j), s = (F)__ldg(cs + half + j);
-  const F y = row[o];
+  const F y = (F)row[o];
   return first ? x * c - y * s : x * c + y * s;
 }
 
