@@ -409,9 +409,12 @@ AQUA_API int aqua_paged_status(const aqua_paged_cache* cache, int* status_out, a
  * that, and when it grows the codes it holds are re-coded (multiplied by the
  * ratio of the scales, nearest even: exact but for values that become
  * subnormal).  Slots after the appended tokens are left as they were.
- * Infinities saturate at 448 s, NaN stays NaN.
+ * Infinities saturate at 448 s, NaN stays NaN (a key row that holds an infinity
+ * before the projection may become NaN as a whole).
  * Appending a run at once or token by token gives the same values but for those
- * subnormals.  A sequence whose run does not fit (or lies outside the rotation
+ * subnormals and for sums within f32 rounding of a tie: single tokens are
+ * projected in f64, short runs in f32, long ones on the tensor cores with both
+ * factors in two f16 parts, which is as exact as an f32 sum.  A sequence whose run does not fit (or lies outside the rotation
  * table, or whose cu_new is not ascending within [0, n_tokens]) is left as it
  * was and AQUA_ERR_ARG recorded.
  */

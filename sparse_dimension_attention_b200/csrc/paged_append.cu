@@ -129,9 +129,11 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio, uint32_t by
   return (r & byte_mask) | (w & ~byte_mask);
 }
 
-// Re-codes slots 0 .. fill-1 of a key block ([m][page] bytes) or a value block ([page][D]).
-__device__ void recode_keys(uint8_t* blk, int m, int page_log2, int fill, float ratio, int tid, int nthreads) {
+// Re-codes slots 0 .. fill-1 of a key block ([m][page] bytes) or a value block ([page][D]).  Rare: kept out of
+// the kernels' loops.
+__device__ __noinline__ void recode_keys(uint8_t* blk, int m, int page_log2, int fill, float ratio, int tid, int nthreads) {
   const int page = 1 << page_log2, chunks = (m << page_log2) >> 4;
+#pragma unroll 1
   for (int c = tid; c < chunks; c += nthreads) {
     const int s0 = (c << 4) & (page - 1);
     if (s0 >= fill) continue;
@@ -147,7 +149,8 @@ __device__ void recode_keys(uint8_t* blk, int m, int page_log2, int fill, float 
     *p = w;
   }
 }
-__device__ void recode_values(uint8_t* blk, int fill, float ratio, int tid, int nthreads) {
+__device__ __noinline__ void recode_values(uint8_t* blk, int fill, float ratio, int tid, int nthreads) {
+#pragma unroll 1
   for (int c = tid; c < fill * (D / 16); c += nthreads) {
     uint4* p = reinterpret_cast<uint4*>(blk) + c;
     uint4 w = *p;
@@ -274,6 +277,693 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
     reinterpret_cast<uint32_t*>(vb + (size_t)(fill + t) * D)[lane] =
         f32x4_to_e4m3x4(f[0] * vi, f[1] * vi, f[2] * vi, f[3] * vi);
   }
+}
+
+// ------------------------------------------------------------------ runs of tokens on the tensor cores
+//
+// A tile is 128 slots of a sequence, aligned, so whole pages; persistent blocks,
+// one an SM, each of one head, share the tiles.  k~ = x P on tcgen05 with
+// both factors split into two f16 parts (x_l P_h + x_h P_l + x_h P_h, f32
+// accumulation): rows and P are first brought to [2^10, 2^11) by powers of two,
+// so the parts hold 22 bits and the dropped product is below 2^-22 of a term.
+// The tensor cores cut every sum they extend off to 24 bits, which makes a chain
+// of 24 products, the small ones first, 2.3e-7 off (2-norm): as an f32 sum of
+// 128 terms (2.0e-7; exact sums of the same parts: 0.7e-7).
+//
+// What bounds it is the arithmetic around the products (some 20 instructions an
+// element), so the roles overlap: warps 0-7 rotate, normalise and split the rows
+// of a tile, warps 8-11 turn projected rows into codes, warps 12-19 do the
+// values, one lane issues the products.  Operands and accumulators are double.
+// The loops are kept short (rolled over 32 rows or 32 columns): unrolled, the
+// roles together were 122 KB of code and mostly waited for instructions.
+constexpr int kTile = 128;
+constexpr int kRowThreads = 256, kKeyThreads = 128, kValThreads = 256;
+constexpr int kKeyWarp0 = kRowThreads / 32, kValWarp0 = kKeyWarp0 + kKeyThreads / 32;
+constexpr int kProdWarp = kValWarp0 + kValThreads / 32;
+constexpr int kTileThreads = (kProdWarp + 1) * 32;
+constexpr int kGroups = kTile / 16;        // groups of 16 slots
+constexpr int kPart = kTile * D * 2;       // bytes of one f16 part of a 128 x 128 operand
+enum NamedBar { kBarKey = 1, kBarVal = 2, kBarRow = 3 };
+
+// tiles (128-slot blocks) that a run of n tokens from slot `start` touches
+__device__ __forceinline__ int run_tiles(int start, int n) { return n > 0 ? ((start + n - 1) >> 7) - (start >> 7) + 1 : 0; }
+
+// Tile ti of the run of sequence b.
+struct Walk {
+  int b, start, token, n, ti;
+  __device__ __forceinline__ int base() const { return ((start >> 7) + ti) << 7; }          // first slot of the tile
+  __device__ __forceinline__ int lo() const { return max(start, base()) - base(); }          // new slots of the tile
+  __device__ __forceinline__ int hi() const { return min(start + n, base() + kTile) - base(); }
+  __device__ __forceinline__ void next(const PagedView& c, const AppendParams& a) {         // there is one
+    if (++ti < run_tiles(start, n)) return;
+    ti = 0;
+    do {
+      bool bad;
+      n = run_length(a, c, ++b, token, start, bad);
+    } while (n == 0);
+  }
+  // tokens that the page of slot group g held before: the page the run starts in, when it starts inside
+  __device__ __forceinline__ int held(const PagedView& c, int g) const {
+    return ti == 0 && (base() + 16 * g) >> c.page_log2 == start >> c.page_log2 ? start & ((1 << c.page_log2) - 1) : 0;
+  }
+  // page of slot group g if the run has tokens in it (-1: none, or no such page)
+  __device__ __forceinline__ int page_of(const PagedView& c, int g) const {
+    if (16 * g >= hi() || 16 * g + 16 <= lo()) return -1;
+    const int pid = __ldg(c.table + (size_t)b * c.max_pages + ((base() + 16 * g) >> c.page_log2));
+    if (pid >= 0 && pid < c.n_pages) return pid;
+    report_arg(c);
+    return -1;
+  }
+};
+
+struct TileMisc {
+  uint64_t x_full[2], x_free[2], d_full[2], d_free[2];
+  float unit[4][kTile];                    // power of two that undoes a row's and P's normalisation
+  float kgroup[2][kGroups];                // largest magnitude of every 16 slots, of even and odd tiles
+  float vgroup[kValThreads / 32][kGroups];
+  float vinv[kGroups];                     // 1 / scale of every 16 slots' page
+  int vpid[kGroups];                       // their page, -1: none
+  float vrecode;                           // factor for the codes an open page holds already (1: none)
+  uint32_t pmax;
+  uint32_t tmem;
+  int scan[kTileThreads / 32];
+  Walk at;                                 // the block's first tile
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// two floats as a packed pair of f16, and what the pair leaves
+__device__ __forceinline__ uint32_t split_pair(float& x0, float& x1) {
+  const uint32_t h = pack_half2(x0, x1);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  x0 -= f.x;
+  x1 -= f.y;
+  return h;
+}
+
+// byte offset of eight columns from `col` (a multiple of 8) of a row in a part: two halves of 64 columns, rows
+// of 128 bytes, 128-byte swizzle
+__device__ __forceinline__ uint32_t part_off(int row, int col) {
+  return (uint32_t)((col >> 6) * (kTile * 128) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// 32 columns of this warp's lanes; the registers hold them after tmem_wait_ld
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));                  // not before the wait
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));      // not before the wait
+}
+
+// power of two that brings a largest magnitude f * 2^e to [2^10, 2^11), and its inverse
+__device__ __forceinline__ float norm_up(float mx, float& undo) {
+  const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
+  undo = __uint_as_float((uint32_t)(e - 10 + 127) << 23);
+  return __uint_as_float((uint32_t)(10 - e + 127) << 23);
+}
+
+// eight consecutive elements as f32
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+}
+// the same eight elements, as they lie
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 u, v;
+  __device__ __forceinline__ void load(const float* p) {
+    u = __ldg(reinterpret_cast<const float4*>(p));
+    v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+  }
+  // times a power of two
+  __device__ __forceinline__ void scale(float p) {
+    u = make_float4(u.x * p, u.y * p, u.z * p, u.w * p);
+    v = make_float4(v.x * p, v.y * p, v.z * p, v.w * p);
+  }
+  // largest magnitude, NaN passed over
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))),
+                 fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+  }
+};
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = bf16lo(w.x); f[1] = bf16hi(w.x); f[2] = bf16lo(w.y); f[3] = bf16hi(w.y);
+    f[4] = bf16lo(w.z); f[5] = bf16hi(w.z); f[6] = bf16lo(w.w); f[7] = bf16hi(w.w);
+  }
+  __device__ __forceinline__ void scale(float f) {
+    const __nv_bfloat162 s = __float2bfloat162_rn(f);
+    __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __hmul2(p[i], s);
+  }
+  __device__ __forceinline__ float amax() const {
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+    return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
+  }
+};
+
+// largest finite magnitude of eight elements: the path of rows with an infinity, kept out of the loops
+template <typename T>
+__device__ __noinline__ float finite_amax8(const T* p) {
+  float m = 0.f;
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(Elem<T>::load(p + e)));
+  return m;
+}
+
+// Bounded wait; after a time-out every later wait returns at once and the roles run through their loops (all
+// named barriers are met), writing garbage in bounds.
+__device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, TileMisc& ms, int32_t* ctrl) {
+  if (!mbar_try_wait(bar, parity) && !*(volatile int*)&ms.abort && !mbar_wait_bounded(bar, parity)) {
+    *(volatile int*)&ms.abort = 1;
+    record_status(ctrl, AQUA_ERR_TIMEOUT);
+  }
+  __syncwarp();
+}
+
+// How a row is rotated: pairs (i, i + rot / 2) or (2 i, 2 i + 1) in blocks of eight (rot a multiple of 16, or no
+// rotation), or dim by dim.  One kernel for each: three roles' loops share the instruction cache, and a
+// kernel that held all three forms waited for instructions most of the time.
+enum RotMode { kHalves = 0, kPairs = 1, kAnyRot = 2 };
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(PagedView c, AppendParams a) {
+  extern __shared__ __align__(1024) uint8_t tile_smem[];
+  uint8_t* const sP = tile_smem;                         // P: two f16 parts
+  uint8_t* const sX = sP + 2 * kPart;                    // rows: two f16 parts, two buffers
+  uint8_t* const sC = sX + 4 * kPart;                    // codes of a tile's keys, as its pages hold them; two buffers
+  TileMisc& ms = *reinterpret_cast<TileMisc*>(sC + 2 * D * kTile);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
+
+  if (tid == 0) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.x_full[i], kRowThreads);
+      mbar_init(&ms.x_free[i], 1);
+      mbar_init(&ms.d_full[i], 1);
+      mbar_init(&ms.d_free[i], kKeyThreads);
+    }
+    fence_barrier_init();
+    ms.abort = 0;
+    ms.pmax = 0;
+  }
+  if (w == kProdWarp) {
+    // 128 columns for each of two tiles
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)), "r"(256u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = ms.tmem;
+  // ---- P of the head, normalised and split (before the wait: the kernel before does not write it)
+  float p_undo;
+  {
+    constexpr int kEach = (D * D / 8 + kTileThreads - 1) / kTileThreads;
+    Raw8<float> f[kEach];
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kTileThreads;
+      if (e < D * D / 8) f[i].load(a.P + (size_t)h * D * D + 8 * e);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (tid + i * kTileThreads < D * D / 8) mx = fmaxf(mx, f[i].amax());
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    if (lane == 0) atomicMax(&ms.pmax, __float_as_uint(mx));
+    __syncthreads();
+    const float up = norm_up(__uint_as_float(ms.pmax), p_undo);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kTileThreads, row = e >> 4, col = (e & 15) * 8;
+      if (e >= D * D / 8) break;
+      float x[8];
+      f[i].scale(up);
+      f[i].get(x);
+      uint32_t hw[4], lw[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        // columns past d_store are not stored: zeros, so that they set no maximum
+        float x0 = col + 2 * y < c.m ? x[2 * y] : 0.f, x1 = col + 2 * y + 1 < c.m ? x[2 * y + 1] : 0.f;
+        hw[y] = split_pair(x0, x1);
+        lw[y] = pack_half2(x0, x1);
+      }
+      *reinterpret_cast<uint4*>(sP + part_off(row, col)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(sP + kPart + part_off(row, col)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    }
+    fence_proxy_async_smem();
+  }
+
+  pdl_wait();
+  // ---- this block's share of the tiles: exclusive sums of the runs' tiles, a pass per kTileThreads sequences
+  int n_tiles = 0, i0 = 0, n_my = 0;
+  Walk at = {0, 0, 0, 0, 0};
+  const bool once = c.B <= kTileThreads;     // one pass finds the total and, from the same registers, the first tile
+#pragma unroll 1
+  for (int round = 0; round < (once ? 1 : 2); ++round) {
+    int before = 0;
+#pragma unroll 1
+    for (int base = 0; base < c.B; base += kTileThreads) {
+      Walk mine = {base + tid, 0, 0, 0, 0};
+      int x = 0;
+      if (mine.b < c.B) {
+        bool bad;
+        mine.n = run_length(a, c, mine.b, mine.token, mine.start, bad);
+        if (bad && blockIdx.x == 0 && round == 0) report_arg(c);
+        x = run_tiles(mine.start, mine.n);
+      }
+      int sum = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      __syncthreads();
+      if (lane == 31) ms.scan[w] = sum;
+      __syncthreads();
+      int off = before, all = 0;
+#pragma unroll
+      for (int y = 0; y < kTileThreads / 32; ++y) {
+        if (y < w) off += ms.scan[y];
+        all += ms.scan[y];
+      }
+      before += all;
+      if (once) n_tiles = all;
+      if (once || round == 1) {
+        i0 = (int)((long long)blockIdx.x * n_tiles / gridDim.x);
+        n_my = (int)((long long)(blockIdx.x + 1) * n_tiles / gridDim.x) - i0;
+        if (x > 0 && i0 >= off + sum - x && i0 < off + sum) {
+          mine.ti = i0 - (off + sum - x);
+          ms.at = mine;
+        }
+      }
+    }
+    if (!once && round == 0) n_tiles = before;
+  }
+  __syncthreads();
+  if (n_my > 0) at = ms.at;
+
+  if (w < kKeyWarp0) {
+    // ================= rows: rotate, normalise, split =================
+    // eight lanes a row, sixteen dims each: a block of eight rotated pairs, or sixteen dims past the rotation
+    const int j8 = tid & 7, rot = a.rope.cs ? a.rope.rot : 0, half = rot >> 1;
+    const bool turned = 8 * j8 < half, mixed = MODE != kHalves || !turned;
+    const int da = mixed ? 16 * j8 : 8 * j8, db = mixed ? 16 * j8 + 8 : half + 8 * j8;
+    Raw8<T> ra, rb;                                           // one pass ahead
+    Walk ahead = at;
+    int ahead_t = 0, ahead_pass = 0;
+    auto fetch = [&]() {
+      if (ahead_t < n_my) {
+        const int r = (tid >> 3) + 32 * ahead_pass;
+        if (r >= ahead.lo() && r < ahead.hi()) {
+          const T* src = static_cast<const T*>(a.k_new) + (size_t)(ahead.token + ahead.base() + r - ahead.start) * a.ks.row +
+                         (size_t)h * a.ks.head;
+          ra.load(src + da);
+          rb.load(src + db);
+        }
+        if (++ahead_pass == 4) {
+          ahead_pass = 0;
+          if (++ahead_t < n_my) ahead.next(c, a);
+        }
+      }
+    };
+    if (MODE != kAnyRot) fetch();
+#pragma unroll 1
+    for (int t = 0; t < n_my; ++t) {
+      const int buf = t & 1;
+      uint8_t* const X = sX + buf * 2 * kPart;
+      const int base = at.base(), lo = at.lo(), hi = at.hi();
+#pragma unroll 1
+      for (int pass = 0; pass < 4; ++pass) {
+        const int r = (tid >> 3) + 32 * pass;
+        const bool live = r >= lo && r < hi;
+        float x[16], undo, up;
+        float mx = 0.f;                        // of the row before it is rotated: at most sqrt(2) off; NaN is passed over,
+                                               // an infinity makes its row NaN
+        if (MODE != kAnyRot) {
+          if (live) mx = fmaxf(ra.amax(), rb.amax());
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          up = norm_up(mx, undo);
+          if (live) {
+            ra.scale(up);
+            rb.scale(up);
+            ra.get(x);
+            rb.get(x + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+          }
+          fetch();
+          if (live && turned) {
+            const float* cs = a.rope.cs + (size_t)(base + r) * rot + 8 * j8;
+            float cc[8], ss[8];
+            load8(cs, cc);
+            load8(cs + half, ss);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int ia = MODE == kPairs ? 2 * e : e, ib = MODE == kPairs ? 2 * e + 1 : 8 + e;
+              const float u = x[ia], v = x[ib];
+              x[ia] = u * cc[e] - v * ss[e];
+              x[ib] = v * cc[e] + u * ss[e];
+            }
+          }
+        } else {
+          const T* src = static_cast<const T*>(a.k_new) + (size_t)(at.token + base + r - at.start) * a.ks.row +
+                         (size_t)h * a.ks.head;
+          const float* cs = a.rope.cs + (size_t)(base + r) * rot;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int i = 16 * j8 + e;
+            float v = live ? Elem<T>::load(src + i) : 0.f;
+            if (live && i < rot) {
+              const bool first = a.rope.interleaved ? (i & 1) == 0 : i < half;
+              const int j = a.rope.interleaved ? i >> 1 : (first ? i : i - half);
+              const int o = a.rope.interleaved ? i ^ 1 : (first ? i + half : i - half);
+              const float cc = __ldg(cs + j), ss = __ldg(cs + half + j), z = Elem<T>::load(src + o);
+              v = first ? v * cc - z * ss : v * cc + z * ss;
+            }
+            x[e] = v;
+            mx = fmaxf(mx, fabsf(v));
+          }
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          up = norm_up(mx, undo);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] *= up;
+        }
+        if (pass == 0 && t >= 2) tile_wait(&ms.x_free[buf], ((t - 2) >> 1) & 1, ms, c.ctrl);
+        if (j8 == 0) ms.unit[t & 3][r] = undo * p_undo;
+        uint32_t hw[8], lw[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          hw[e] = split_pair(x[2 * e], x[2 * e + 1]);
+          lw[e] = pack_half2(x[2 * e], x[2 * e + 1]);
+        }
+        *reinterpret_cast<uint4*>(X + part_off(r, da)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(X + part_off(r, db)) = make_uint4(hw[4], hw[5], hw[6], hw[7]);
+        *reinterpret_cast<uint4*>(X + kPart + part_off(r, da)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        *reinterpret_cast<uint4*>(X + kPart + part_off(r, db)) = make_uint4(lw[4], lw[5], lw[6], lw[7]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ms.x_full[buf]);
+      if (t + 1 < n_my) at.next(c, a);
+    }
+  } else if (w == kProdWarp) {
+    // ================= products =================
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+#pragma unroll 1
+      for (int t = 0; t < n_my; ++t) {
+        const int buf = t & 1;
+        bool ok = mbar_wait_bounded(&ms.x_full[buf], (t >> 1) & 1);
+        if (ok && t >= 2) ok = mbar_wait_bounded(&ms.d_free[buf], ((t - 2) >> 1) & 1);
+        if (!ok) {
+          if (!*(volatile int*)&ms.abort) record_status(c.ctrl, AQUA_ERR_TIMEOUT);
+          *(volatile int*)&ms.abort = 1;
+          break;
+        }
+        fence_proxy_async_smem();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t xa = smem_u32(sX) + buf * 2 * kPart, pa = smem_u32(sP);
+#pragma unroll
+        for (int pr = 0; pr < 3; ++pr) {     // x_l P_h, x_h P_l, x_h P_h: the small ones first
+          const uint64_t ad = desc_sw128(xa + (pr == 0 ? kPart : 0), 16);
+          const uint64_t bd = desc_sw128(pa + (pr == 1 ? kPart : 0), kTile * 128);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_f16(tmem + buf * D, ad + (uint64_t)(((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                    bd + (uint64_t)((ks * 16 * 128) >> 4), idesc, pr > 0 || ks > 0);
+        }
+        commit_to(&ms.x_free[buf]);
+        commit_to(&ms.d_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (w < kValWarp0) {
+    // ================= projected keys: scales, codes, pages =================
+    const int kt = tid - kKeyWarp0 * 32, kr = 32 * (w & 3) + lane, kg = kr >> 4;           // slot, its group of 16
+    const int per = 1 << (c.page_log2 - 4), g0 = kg & ~(per - 1), mask = (1 << c.page_log2) - 1;
+    const uint32_t bytes = (uint32_t)c.m << c.page_log2, block = (uint32_t)((c.m + 31) & ~31) << c.page_log2;   // of a page's keys
+#pragma unroll 1
+    for (int t = 0; t < n_my; ++t) {
+      const int buf = t & 1, lo = at.lo(), hi = at.hi();
+      // this slot's page; the page the run starts inside (uniform), with its old scale, read before anyone changes it
+      const int pid = at.page_of(c, kg);
+      const int open_fill = at.held(c, lo >> 4), open = open_fill > 0 ? at.page_of(c, lo >> 4) : -1;
+      const float open_scale = open >= 0 ? c.ks[(size_t)open * c.Hkv + h] : 0.f;
+      tile_wait(&ms.d_full[buf], (t >> 1) & 1, ms, c.ctrl);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      // tensor memory is read twice, for the maxima and for the codes: 128 numbers do not fit the registers
+      const uint32_t col = tmem + ((uint32_t)(32 * (w & 3)) << 16) + buf * D;
+      const float unit = ms.unit[t & 3][kr];
+      float km = 0.f;
+#pragma unroll 1
+      for (int q = 0; q < D; q += 64) {
+        uint32_t x[32], y[32];
+        tmem_ld32(col + q, x);
+        tmem_ld32(col + q + 32, y);
+        tmem_wait_ld(x, y);
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(y[e]))));
+        if (!(m * unit < INFINITY)) {        // an infinity among them: the largest finite one
+          m = 0.f;
+#pragma unroll 1
+          for (int e = 0; e < 64; ++e) {
+            uint32_t z;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                         : "=r"(z) : "r"(col + q + e) : "memory");
+            if (fabsf(__uint_as_float(z)) * unit < INFINITY) m = fmaxf(m, fabsf(__uint_as_float(z)));
+          }
+        }
+        km = fmaxf(km, m);
+      }
+      km *= unit;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
+      if ((lane & 15) == 0) ms.kgroup[buf][kg] = km;
+      named_bar_sync(kBarKey, kKeyThreads);  // the other buffer's readers are past the next barrier by the time it is reused
+#pragma unroll 1
+      for (int g = g0; g < g0 + per; ++g) km = fmaxf(km, ms.kgroup[buf][g]);
+      const float s = page_scale(km, open_scale, pid == open ? open_fill : 0), f = unit / s;
+      uint8_t* const codes = sC + buf * (D * kTile);
+      {
+        uint8_t* dst = codes + (uint32_t)(kr >> c.page_log2) * block + (kr & mask);
+        const int row = 1 << c.page_log2;    // bytes from a dimension to the next
+#pragma unroll 1
+        for (int q = 0; q < c.m; q += 32) {
+          uint32_t x[32];
+          tmem_ld32(col + q, x);
+          tmem_wait_ld(x);
+          uint8_t* d = dst + q * row;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {  // dims past d_store fall into the buffer's padding
+            const uint16_t code = f32x2_to_e4m3x2(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f);
+            d[e * row] = (uint8_t)code;
+            d[(e + 1) * row] = (uint8_t)(code >> 8);
+          }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive(&ms.d_free[buf]);
+      }
+      // one thread of each page writes its scale: that of the page's first slot in the tile, or the run's first
+      const int first = max(lo, 16 * g0);
+      if (kr == first && kr < hi && pid >= 0) c.ks[(size_t)pid * c.Hkv + h] = s;
+      if (open >= 0) {                       // what the open page holds follows its scale
+        const int o0 = (lo >> 4) & ~(per - 1);
+        float om = 0.f;
+#pragma unroll 1
+        for (int g = o0; g < o0 + per; ++g) om = fmaxf(om, ms.kgroup[buf][g]);
+        const float now = page_scale(om, open_scale, open_fill);
+        if (now != open_scale)
+          recode_keys(c.k + c.kblock(open, h), c.m, c.page_log2, open_fill, open_scale / now, kt, kKeyThreads);
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(kBarKey, kKeyThreads);
+      // out: whole pages by one bulk copy each, as they lie; pages with other slots in bytes
+#pragma unroll 1
+      for (int pg = 0; pg < kTile >> c.page_log2; ++pg) {
+        const int s0 = pg << c.page_log2, s1 = s0 + mask + 1;
+        if (s1 <= lo || s0 >= hi) continue;
+        const int pd = at.page_of(c, s0 < lo ? lo >> 4 : s0 >> 4);
+        if (pd < 0) continue;
+        uint8_t* dst = c.k + c.kblock(pd, h);
+        const uint8_t* src = codes + (uint32_t)pg * block;
+        if (s0 >= lo && s1 <= hi) {
+          if (kt == 0)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                         : "memory");
+        } else {
+          const int a0 = max(lo, s0) - s0, a1 = min(hi, s1) - s0, lg = c.page_log2 - 4;
+#pragma unroll 1
+          for (int i = kt; i < c.m << lg; i += kKeyThreads) {                // sixteen slots of a dimension
+            const int x0 = (i & ((1 << lg) - 1)) << 4, x1 = x0 + 16;
+            if (x0 >= a0 && x1 <= a1) {
+              reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+            } else if (x0 < a1 && x1 > a0) {
+#pragma unroll 1
+              for (int x = max(x0, a0); x < min(x1, a1); ++x) dst[16 * i - x0 + x] = src[16 * i - x0 + x];
+            }
+          }
+        }
+      }
+      if (kt == 0) {
+        // the copies of the tile before have read their buffer, which the next tile's codes go to
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 1;" ::: "memory");
+      }
+      if (t + 1 < n_my) at.next(c, a);
+    }
+    if (kt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  } else {
+    // ================= values =================
+    const int vt = tid - kValWarp0 * 32, vw = vt >> 5, col = 8 * (vt & 15);      // sixteen lanes a row: rows 16 i + vt / 16
+#pragma unroll 1
+    for (int t = 0; t < n_my; ++t) {
+      const int base = at.base(), lo = at.lo(), hi = at.hi();
+      // the first warp, four lanes to a group of 16 slots: its page, what that held, its old scale
+      int pid = -1, fill = 0;
+      float old = 0.f;
+      const int vg = vt >> 2;
+      if (vw == 0) {
+        pid = at.page_of(c, vg);
+        fill = at.held(c, vg);
+        if (pid >= 0 && fill > 0) old = c.vs[(size_t)pid * c.Hkv + h];
+      }
+      const T* src = static_cast<const T*>(a.v_new) + (size_t)h * a.vs.head + col;
+      const long long row0 = (long long)at.token + base - at.start;              // input row of slot 0 (may lie before the run)
+      const T* mine = src + (row0 + (vt >> 4)) * a.vs.row;                        // this thread's row of group 0
+      // row i of this thread belongs to group i; bf16 rows stay in registers, of f32 rows every second four are
+      // loaded again for the codes
+      constexpr int kHold = sizeof(T) == 2 ? kGroups : kGroups / 2;
+      Raw8<T> rows[kHold];
+      auto in_run = [&](int i) { return 16 * i + (vt >> 4) >= lo && 16 * i + (vt >> 4) < hi; };
+      auto load_rows = [&](int q) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+          if (in_run(q + i)) rows[i].load(mine + (size_t)(16 * (q + i)) * a.vs.row);
+      };
+#pragma unroll
+      for (int q = 0; q < kGroups; q += kHold) {
+        load_rows(q);
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          float m = in_run(q + i) ? rows[i].amax() : 0.f;
+          if (!(m < INFINITY)) m = finite_amax8(mine + (size_t)(16 * (q + i)) * a.vs.row);
+          const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+          if (lane == 0) ms.vgroup[vw][q + i] = __uint_as_float(u);
+        }
+      }
+      named_bar_sync(kBarVal, kValThreads);
+      if (vw == 0) {
+        static_assert(kGroups * 4 == 32 && kValThreads == 256, "four lanes a group, two warps' maxima each");
+        float m = fmaxf(ms.vgroup[2 * (lane & 3)][vg], ms.vgroup[2 * (lane & 3) + 1][vg]);
+        const int per = 1 << (c.page_log2 - 4);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)     // over the warps' maxima, then over the groups of a page
+          if (o < 4 * per) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = page_scale(m, old, fill);
+        if ((lane & 3) == 0) {
+          ms.vinv[vg] = 1.f / s;
+          ms.vpid[vg] = pid;
+          // one group of each page speaks for it: the page's first, or the run's
+          const bool speaks = pid >= 0 && vg == max(vg & ~(per - 1), lo >> 4);
+          if (speaks) c.vs[(size_t)pid * c.Hkv + h] = s;
+          if (vg == lo >> 4) ms.vrecode = pid >= 0 && fill > 0 ? old / s : 1.f;
+        }
+      }
+      named_bar_sync(kBarVal, kValThreads);
+      {
+        const int og = lo >> 4, open = ms.vpid[og];
+        if (ms.vrecode != 1.f && open >= 0)
+          recode_values(c.v + c.vblock(open, h), at.start & ((1 << c.page_log2) - 1), ms.vrecode, vt, kValThreads);
+      }
+      const int mask = (1 << c.page_log2) - 1;
+#pragma unroll
+      for (int y = 0; y < kGroups; y += kHold) {
+        const int q = kGroups - kHold - y;    // the rows loaded last first
+        if (y > 0) load_rows(q);
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          const int pd = ms.vpid[q + i];
+          if (!in_run(q + i) || pd < 0) continue;
+          const float s = ms.vinv[q + i];
+          float f[8];
+          rows[i].get(f);
+          *reinterpret_cast<uint2*>(c.v + c.vblock(pd, h) + (size_t)((base + 16 * (q + i) + (vt >> 4)) & mask) * D + col) =
+              make_uint2(f32x4_to_e4m3x4(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
+                         f32x4_to_e4m3x4(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+        }
+      }
+      named_bar_sync(kBarVal, kValThreads);
+      if (t + 1 < n_my) at.next(c, a);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (w == kProdWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
+}
+
+template <typename T, int MODE>
+int launch_tiles_as(const PagedView& c, const AppendParams& a, cudaStream_t st) {
+  const int smem = 6 * kPart + 2 * D * kTile + (int)sizeof(TileMisc);
+  const int rc = set_smem_limit(paged_append_tile_kernel<T, MODE>, smem, "paged_append_tile_kernel");
+  if (rc != AQUA_OK) return rc;
+  // a run of n >= 1 tokens touches at most (n - 2) / 128 + 2 tiles, and at most n
+  const long long by_tile = a.n_tokens / kTile + 2LL * c.B, most = by_tile < a.n_tokens ? by_tile : a.n_tokens;
+  const int each = device_sm_count() / c.Hkv > 0 ? device_sm_count() / c.Hkv : 1;      // blocks a head
+  const cudaError_t e = launch_pdl(paged_append_tile_kernel<T, MODE>, dim3((unsigned)(most < each ? most : each), c.Hkv),
+                                   dim3(kTileThreads), smem, st, c, a);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_append_tile_kernel: %s", cudaGetErrorString(e));
+  return check_launch("paged_append_tile_kernel");
+}
+template <typename T>
+int launch_tiles(const PagedView& c, const AppendParams& a, cudaStream_t st) {
+  if (a.rope.cs == nullptr) return launch_tiles_as<T, kHalves>(c, a, st);
+  if (a.rope.rot % 16 != 0) return launch_tiles_as<T, kAnyRot>(c, a, st);
+  return a.rope.interleaved ? launch_tiles_as<T, kPairs>(c, a, st) : launch_tiles_as<T, kHalves>(c, a, st);
 }
 
 // One new token for each sequence: a block takes up to kStepGroup sequences of one
@@ -424,6 +1114,15 @@ int launch_paged_append(const PagedView& c, const void* k_new, const void* v_new
   a.k_new = k_new; a.v_new = v_new; a.ks = ks; a.vs = vs; a.start = start; a.cu = cu;
   a.P = P; a.rope = rope; a.n_tokens = n_tokens;
   if (cu == nullptr) return bf16 ? launch_step<__nv_bfloat16>(c, a, st) : launch_step<float>(c, a, st);
+  // Estimates in ns, from both kernels measured over 1 to 128 runs of 16 to 512 tokens, pages of 16 to 128 and 1 and
+  // 8 heads.  CUDA cores: 0.3 us a token, of a page's worth of one block or of an SM's share; tiles: a fixed 10 us
+  // and 5.5 us for every further tile of an SM, however few of its rows are used.  (64 tokens of one sequence, 8
+  // heads, pages of 64: 21.5 us against 17; 16 tokens: 7.5 against 13.)
+  const long long sms = device_sm_count(), run = n_tokens / c.B + 1, page = 1 << c.page_log2;
+  const long long share = n_tokens * (long long)c.Hkv / sms, most = run < page ? run : page;
+  const long long cores = 4000 + 300 * (share > most ? share : most);
+  const long long tiles = 10000 + 5500 * ((n_tokens / kTile + c.B) * (long long)c.Hkv / sms);
+  if (tiles < cores) return bf16 ? launch_tiles<__nv_bfloat16>(c, a, st) : launch_tiles<float>(c, a, st);
   return bf16 ? launch_run<__nv_bfloat16>(c, a, st) : launch_run<float>(c, a, st);
 }
 

@@ -168,6 +168,95 @@ def test_append_runs(Hkv, page, m, dtype, rope, start, new):
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
 
 
+@pytest.mark.parametrize("Hkv,page,m,dtype,rope,start,new", [
+    (16, 16, 128, "bf16", (128, False), [3, 0, 127], [260, 100, 129]),      # 128-slot tiles of eight pages, ends inside
+    (16, 16, 100, "f32", (128, True), [16, 5], [255, 250]),
+    (16, 32, 33, "bf16", (36, False), [0, 31, 40], [300, 1, 180]),          # rotations that are no multiple of 16
+    (8, 64, 96, "f32", (6, True), [60, 0], [500, 64]),
+    (4, 128, 128, "bf16", None, [0, 130], [256, 400]),                      # whole pages only, then partial ones
+    (2, 64, 128, "f32", (48, False), [0, 1, 0], [2000, 0, 63]),             # many tiles a block
+    (150, 32, 16, "bf16", (32, True), [7], [90]),                           # more heads than SMs
+])
+def test_append_long_runs(Hkv, page, m, dtype, rope, start, new):
+    """Runs that go to the tensor-core tiles."""
+    test_append_runs(Hkv, page, m, dtype, rope, start, new)
+
+
+def test_append_long_runs_of_many_sequences():
+    """More sequences than one pass of the tile kernel's scan, runs of 0 to 60 tokens, rows of very different size,
+    the page's scale growing where a run continues one."""
+    rng = np.random.default_rng(30)
+    Hkv, page, m, B = 16, 32, 20, 700
+    _, P32 = calib_P(Hkv)
+    start = [int(x) for x in rng.integers(0, 70, B)]
+    new = [int(x) for x in rng.integers(0, 61, B)]
+    cache = make_cache(B, Hkv, page, m, 5, seed=31)
+    n = sum(new)
+    k, v = rows_of(rng, n, Hkv, "bf16", 4.0), rows_of(rng, n, Hkv, "bf16", 4.0)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    before = snap(cache)
+    aq.aqua_paged_append(cache.desc, tdev(k, torch.bfloat16), tdev(v, torch.bfloat16),
+                         torch.tensor(start, dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=torch.from_numpy(cu).cuda())
+    check_append(cache, before, k, v, P32, start, cu, None, False)
+    assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+def test_append_long_runs_bad_device_data():
+    """Long runs with a page that does not exist, one that does not fit, one before the first slot: those tokens are
+    skipped and reported, the others are right."""
+    rng = np.random.default_rng(34)
+    Hkv, page, m, new, start = 8, 64, 128, [200, 200, 200, 300], [0, 10, 100, -1]
+    _, P32 = calib_P(Hkv)
+    cache = make_cache(4, Hkv, page, m, 4, seed=35)
+    cache.block_table[1, 1] = cache.n_pages
+    n = sum(new)
+    k, v = rows_of(rng, n, Hkv, "bf16"), rows_of(rng, n, Hkv, "bf16")
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    before = snap(cache)
+    aq.aqua_paged_append(cache.desc, tdev(k, torch.bfloat16), tdev(v, torch.bfloat16),
+                         torch.tensor(start, dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=torch.from_numpy(cu).cuda())
+    after = snap(cache)
+    for p0 in (0, 2, 3):                     # the pages of sequence 1 that exist were written
+        p = int(before["block_table"][1, p0])
+        assert not np.array_equal(before["v_pages"][p], after["v_pages"][p])
+        for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+            before[name][p] = after[name][p]
+    check_append(cache, before, k, v, P32, start, cu, None, False, skip=(1, 2, 3))      # 2: 100 + 200 > 256
+    assert aq.aqua_paged_status(cache.desc) == aq.abi.AQUA_ERR_ARG
+
+
+def test_append_long_run_with_infinities():
+    """Values: infinities saturate and NaN stays, the finite numbers set the scales.  A key row with an infinity
+    spoils no other row."""
+    Hkv, page, m, n = 8, 64, 128, 300
+    rng = np.random.default_rng(32)
+    _, P32 = calib_P(Hkv)
+    cache = make_cache(1, Hkv, page, m, 5, seed=33)
+    k, v = rows_of(rng, n, Hkv, "f32"), rows_of(rng, n, Hkv, "f32")
+    v[10, 2, 5], v[10, 2, 6], v[200, 0, 127], k[100, 3, 7] = np.inf, -np.inf, np.nan, np.inf
+    before = snap(cache)
+    aq.aqua_paged_append(cache.desc, tdev(k), tdev(v), torch.zeros(1, dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    after = snap(cache)
+    table = after["block_table"][0]
+    vals = lambda name, t, h: PO.e4m3_decode(after[name + "_pages"][table[t // page], h][..., t % page] if name == "k"
+                                             else after[name + "_pages"][table[t // page], h][t % page])
+    for t in range(n):
+        for h in range(Hkv):
+            s = float(after["v_scale"][table[t // page], h])
+            np.testing.assert_array_equal(vals("v", t, h), PO.e4m3_round(v[t, h] / s))
+    for p0 in range(5):
+        for h in range(Hkv):
+            rows = slice(p0 * page, min(n, p0 * page + page))
+            assert float(after["v_scale"][table[p0], h]) == PO.page_scale(PO.finite_max(v[rows, h]))
+    kt = np.einsum("nhi,hij->nhj", np.where(np.isfinite(k), k, 0), P32.astype(np.float64))
+    for t in (99, 101, 64, 127):
+        s = float(after["k_scale"][table[t // page], 3])
+        assert np.all(np.abs(vals("k", t, 3) * s - kt[t, 3]) <= np.maximum(2.0 ** -4 * np.abs(kt[t, 3]), 2.0 ** -10 * s) * 1.0001)
+
+
 @pytest.mark.parametrize("runs", [False, True])
 def test_append_growing_scale_recodes_the_page(runs):
     """Tokens that get larger and larger: the open page's scale grows each time and its codes follow."""
