@@ -10,7 +10,7 @@ namespace aqua {
 int launch_paged_append(const PagedView& c, const void* k_new, const void* v_new, bool bf16, const Strides& ks,
                         const Strides& vs, int n_tokens, const int32_t* start, const int32_t* cu, const float* P,
                         const RopeView& rope, cudaStream_t st);
-size_t paged_decode_workspace_bytes(int n_units, int G);
+size_t paged_decode_workspace_bytes(int B, int Hkv, int G);
 int launch_paged_decode(const PagedView& c, const int32_t* len, const void* q, bool bf16, const Strides& qs,
                         const float* P, const RopeView& rope, int Hq, int k, float scale, void* out, bool out_bf16,
                         int32_t* sel_out, float* qproj_out, float* lse_out, void* ws, cudaStream_t st);
@@ -42,6 +42,9 @@ int validate(const aqua_paged_cache* c) {
                      c->max_pages);
   if (c->Hkv > 65535 || (long long)c->B * c->Hkv > (1LL << 24))
     return set_error(AQUA_ERR_UNSUPPORTED, "paged cache: B*Hkv too large");
+  // rows of the value pages are counted in 31 bits (256 GB of them)
+  if ((long long)c->n_pages * c->Hkv > (1LL << 31) / c->page_size - 1)
+    return set_error(AQUA_ERR_UNSUPPORTED, "paged cache: n_pages * Hkv * page_size over 2^31");
   // slots of a sequence are counted in 32 bits
   if ((long long)c->max_pages * c->page_size > (1LL << 30))
     return set_error(AQUA_ERR_UNSUPPORTED, "paged cache: max_pages * page_size over 2^30 tokens");
@@ -141,7 +144,7 @@ int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new, const vo
 
 size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq) {
   if (validate(cache) != AQUA_OK || Hq < 1 || Hq % cache->Hkv != 0 || Hq / cache->Hkv > kMaxPagedG) return 0;
-  return aqua::paged_decode_workspace_bytes(cache->B * cache->Hkv, Hq / cache->Hkv);
+  return aqua::paged_decode_workspace_bytes(cache->B, cache->Hkv, Hq / cache->Hkv);
 }
 
 int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,
@@ -170,7 +173,7 @@ int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, co
     return set_error(AQUA_ERR_ARG, "%s: len, sel_out, qproj_out and lse_out must be 4-byte aligned", who);
   aqua::Strides qs;
   if ((rc = check_strides(q_stride, q_head_stride, Hq, io_dtype, who, "q", &qs)) != AQUA_OK) return rc;
-  const size_t need = aqua::paged_decode_workspace_bytes(cache->B * cache->Hkv, G);
+  const size_t need = aqua::paged_decode_workspace_bytes(cache->B, cache->Hkv, G);
   if (workspace_bytes < need)
     return set_error(AQUA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
   if (!(scale > 0.f)) scale = 1.0f / std::sqrt((float)cache->d);

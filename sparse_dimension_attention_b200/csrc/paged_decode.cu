@@ -2,11 +2,14 @@
 //
 // paged_select_kernel, one block per (sequence b, KV head g): for the group's
 // query heads q~ = rope(q, len - 1) P (f64, rounded once), the k largest |q~_j|
-// (ties to the lower j), the union U of the kept dimensions, and the masked
-// queries in the layout the tensor cores take them.
+// (ties to the lower j), the union U of the kept dimensions as a bit mask, and the
+// masked queries in the layout the tensor cores take them.
 //
 // paged_attend_kernel, persistent: the tokens of all (b, g) are cut into tiles
-// of 128 and the flat sequence of tiles is split evenly over the blocks.
+// of 128, the flat sequence of tiles into pieces.  Every block has one piece, with
+// five eighths of the work together; the rest are smaller pieces that a block
+// takes when it is done (equal shares left the slowest block 15 to 20 % behind
+// the median).  Short jobs have equal shares only.
 //
 //   s_t  = ks(page) sum_{j in U} q~_j code_t[j] / sqrt(d)
 //   w_t  = s_t log2(e) + log2 vs(page),   p_t = 2^(w_t - M),  M a lazily raised max of w
@@ -29,11 +32,16 @@
 // for 131072 tokens x 8 heads against 41 us of memory time.)
 //
 // Warps 0-3 own one token a thread: scores from tensor memory, softmax, parts of
-// p to shared memory.  Warp 4 issues the products.  Warps 5-8 gather: key rows
-// and value rows in 16-byte pieces from whatever page holds them, written in the
-// 128-byte swizzle the products read; three tiles of 32 KB, two blocks an SM.
-// A block that starts or ends inside a (b, g) writes (M, l, O);
-// paged_merge_kernel adds the parts in block order, so results do not depend on timing.
+// p to shared memory.  Warp 4 issues the products.  Warp 5 walks the pieces and
+// has the value rows brought by tensor copies, one a page.  Warps 6-9 gather the
+// key rows in U (zeros for those no head kept) in 16-byte pieces, 16 tokens of a dim
+// each, in the same 128-byte swizzle.  A key buffer is free as soon as its scores
+// are, a value buffer only after the softmax and its product, a path of 9000 cycles:
+// two key and four value buffers of 16 KB, two blocks an SM.  The first tiles are
+// fetched while the selection still runs, with all their key rows.
+// A piece that starts or ends inside a (b, g) leaves (M, l, O); paged_merge_kernel
+// adds the parts in the order of the tokens.  Which block took a piece changes
+// nothing, so results do not depend on timing.
 //
 // edgentiq, "How AQUA Works", Online Inference: scores on the selected
 // dimensions, softmax, weighted sum of the unprojected values.
@@ -48,10 +56,10 @@ namespace {
 constexpr int D = kHeadDim;
 constexpr int TT = 128;                    // tokens per tile
 constexpr int kSoftThreads = 128;         // one thread per token of a tile
-constexpr int kMmaWarp = 4, kCopyWarp0 = 5;
-constexpr int kCopyThreads = 128;
-constexpr int kThreads = (kCopyWarp0 + kCopyThreads / 32) * 32;
-constexpr int kStages = 3;
+constexpr int kMmaWarp = 4, kValWarp = 5, kKeyWarp0 = 6;
+constexpr int kKeyThreads = 128;
+constexpr int kThreads = kKeyWarp0 * 32 + kKeyThreads;
+constexpr int kVStages = 4, kKStages = 2;
 constexpr int kMaxG = 8;
 constexpr int kSelThreads = 512;
 
@@ -70,19 +78,16 @@ struct DecodeP {
   float* lse_out;
   int32_t* ctrl;
   // workspace
-  int32_t* ucount;       // [n_units] kept rows
-  uint8_t* ulist;        // [n_units][D] kept rows, see ulist_slot
-  uint8_t* qpart;        // [n_units][N][D] e4m3 parts of the masked queries: row h * parts + i, columns in union order
+  uint4* umask;          // [n_units] the dims any head of the group kept
+  uint8_t* qpart;        // [n_units][N][D] e4m3 parts of the masked queries: row h * stride + part
   float* qfac;           // [n_units][kMaxG] factor of a head's scores (log2 domain, without the key scale)
-  float2* part_ml;       // [2 * blocks][kMaxG] (M, l) of a partial result
-  float* part_o;         // [2 * blocks][kMaxG][D]
-  int4* split;           // [blocks] block x starts inside unit .x, whose tiles lie in blocks .y ... .z; .w: slot of
-                         // block .y's part; .x < 0: x starts with a unit
+  int32_t* prefix;       // [B + 1] tiles of one KV head before each sequence
+  int32_t* ctl;          // [0] pieces taken beyond the first ones, [1] pieces in all
+  float2* part_ml;       // [2 * pieces][G] (M, l) of a partial result
+  float* part_o;         // [2 * pieces][G][D]
+  int4* split;           // [pieces] piece x starts inside unit .x, whose tiles lie in pieces .y ... .z; .w: slot of
+                         // piece .y's part; .x < 0: x starts with a unit
 };
-
-// Row r of the union is loaded by threads r % 16 (groups of eight threads), as
-// that group's row r / 16: the eight rows of a group lie side by side.
-__device__ __forceinline__ int ulist_slot(int r) { return (r & 15) * 8 + (r >> 4); }
 
 __device__ __forceinline__ int n_tiles(int len) { return (len + TT - 1) / TT; }
 
@@ -117,7 +122,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   uint32_t (*key)[D] = reinterpret_cast<uint32_t (*)[D]>(&qd[0][0]);
   __shared__ uint32_t kept[GP][4];
   __shared__ float qmul[GP];
-  __shared__ int urow[D];
+  __shared__ int before;
   const int u = blockIdx.x, b = u / c.Hkv, g = u % c.Hkv;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int j = tid & 127, sl = tid >> 7;
@@ -133,7 +138,10 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   const int len = __ldg(p.len + b);
   bool bad;
   const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
-  if (tid == 0 && bad) report_arg(c);
+  if (tid == 0) {
+    if (bad) report_arg(c);
+    if (u == 0) p.ctl[0] = 0;
+  }
   const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
   for (int i = tid; i < GP * D; i += kSelThreads)
     raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
@@ -208,24 +216,15 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
       qs[hh][j] = 0.f;
     }
   }
-  if (tid < D) {
-    uint32_t um[4];
-#pragma unroll
-    for (int wd = 0; wd < 4; ++wd) {
-      um[wd] = 0;
-      for (int hh = 0; hh < G; ++hh) um[wd] |= kept[hh][wd];
+  if (tid == 0) {
+    uint4 um = make_uint4(0, 0, 0, 0);
+    for (int hh = 0; hh < G; ++hh) {
+      um.x |= kept[hh][0];
+      um.y |= kept[hh][1];
+      um.z |= kept[hh][2];
+      um.w |= kept[hh][3];
     }
-    const int count = __popc(um[0]) + __popc(um[1]) + __popc(um[2]) + __popc(um[3]);
-    urow[tid] = -1;
-    named_bar_sync(1, D);
-    if ((um[tid >> 5] >> (tid & 31)) & 1u) {
-      int r = __popc(um[tid >> 5] & ((1u << (tid & 31)) - 1u));
-      for (int x = 0; x < (tid >> 5); ++x) r += __popc(um[x]);
-      urow[r] = tid;
-    }
-    named_bar_sync(1, D);
-    p.ulist[(size_t)u * D + ulist_slot(tid)] = (uint8_t)(urow[tid] < 0 ? 0 : urow[tid]);
-    if (tid == 0) p.ucount[u] = count;
+    p.umask[u] = um;
   }
   __syncthreads();
   if (w < G) {
@@ -245,14 +244,28 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
   // most half a step, so 16 times it stays in range)
   for (int i = tid; i < NH * D; i += kSelThreads) {
-    const int hh = i >> 7, d = urow[j];
-    float x = hh < G && d >= 0 ? qs[hh][d] * qmul[hh] : 0.f;
+    const int hh = i >> 7;
+    float x = hh < G ? qs[hh][j] * qmul[hh] : 0.f;
     if (!(fabsf(x) < INFINITY)) x = NAN;      // an infinite query makes its scores NaN, not the largest code
     uint8_t* dst = p.qpart + ((size_t)u * NH + hh) * stride * D + j;
     for (int y = 0; y < stride; ++y) {
       const uint16_t code = y < parts ? f32x2_to_e4m3x2(x, 0.f) : (uint16_t)0;
       dst[y * D] = (uint8_t)code;
       x = (x - e4m3x2_to_f32x2(code).x) * 16.f;
+    }
+  }
+  // tiles of the sequences before this one (one block of each sequence)
+  if (g == 0) {
+    if (tid == 0) before = 0;
+    __syncthreads();
+    int sum = 0;
+    for (int x = tid; x < b; x += kSelThreads) sum += n_tiles(seq_tokens(c, p, x));
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0 && sum != 0) atomicAdd(&before, sum);
+    __syncthreads();
+    if (tid == 0) {
+      p.prefix[b] = before;
+      if (b == c.B - 1) p.prefix[c.B] = before + n_tiles(n);
     }
   }
   // an empty sequence has no tiles: attention over no token is 0 with lse -inf
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
 // attention
 // ============================================================================
 
-constexpr int kStageV = D * TT;                       // bytes of a tile's value rows, ahead of its key rows
+constexpr int kStageV = D * TT;                       // bytes of a tile's value rows
 
 // Position in the flat sequence of tiles.
 struct Cursor {
@@ -277,12 +290,50 @@ struct Cursor {
   int tile;                // tile of the unit
 };
 
+// The flat sequence of `total` tiles as pieces: nb first ones, then smaller ones.
+struct Pieces {
+  long long total, nb;
+  long long first, rest;   // tiles of a first piece and of a later one; first = 0: equal shares, nothing else
+  __device__ __forceinline__ Pieces(long long t, int blocks) : total(t), nb(min((long long)blocks, t)), first(0), rest(1) {
+    // worth it from eight tiles a block on: three later pieces each
+    if (nb > 0 && total >= 8 * nb) {
+      first = total * 5 / 8 / nb;
+      const long long left = total - first * nb;
+      rest = (left + 3 * nb - 1) / (3 * nb);
+    }
+  }
+  __device__ __forceinline__ long long start(long long p) const {
+    if (first == 0) return p * total / nb;
+    return p <= nb ? p * first : min(total, nb * first + (p - nb) * rest);
+  }
+  __device__ __forceinline__ int of(long long tile) const {
+    if (first == 0) return (int)(((tile + 1) * nb - 1) / total);
+    return (int)(tile < nb * first ? tile / first : nb + (tile - nb * first) / rest);
+  }
+  __device__ __forceinline__ int count() const {
+    return (int)(first == 0 ? nb : nb + (total - nb * first + rest - 1) / rest);
+  }
+};
+
+// What a tile is: written by the value warp when it issues its copies.
+struct TileInfo {
+  int b, g, u, len, tile;
+  int slot;                // where the piece's part of this unit goes; < 0: the piece has the whole unit
+  int q;                   // buffer with the unit's queries
+  int flags;
+};
+enum TileFlag { kFirst = 1, kLast = 2, kEnd = 4 };   // of the piece's part of a unit; of the block's work
+
 struct AttendMisc {
-  uint64_t full[kStages], empty[kStages];   // a stage's copies landed / its products are done
+  uint64_t known[kVStages];                 // a tile's info is written
+  uint64_t v_full[kVStages], v_empty[kVStages];   // value rows landed / their product is done
+  uint64_t k_full[kKStages], k_empty[kKStages];   // key rows, scales and queries landed / the scores are done
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t drain;
-  float ks[kStages][TT / 16];      // key scale of every 16 tokens; negative: their page does not exist
-  float vs[kStages][TT / 16];
+  TileInfo info[kVStages];
+  int stop[2];                     // softmax threads leave after this (even, odd) tile
+  float ks[kVStages][TT / 16];     // key scale of every 16 tokens; negative: their page does not exist
+  float vs[kVStages][TT / 16];
   float red[4][kMaxG];
   long long scan[kThreads / 32];
   Cursor cur;
@@ -294,16 +345,20 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// the box of the map from row y on, to shared memory
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // ------------------------------------------------------------------ tcgen05 wrappers
@@ -360,9 +415,9 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
 }
 
-// Bounded wait that gives up at once when another role did; the first to give up reports.  The copy and
-// softmax threads go on through their loops after that (every later wait returns at once), so that
-// no barrier or shuffle among them is left waiting; what they write then is garbage, in bounds.
+// Bounded wait that gives up at once when another role did; the first to give up reports.  The value warp and
+// the softmax threads go on to a point where all of them leave (every later wait returns at once), so that
+// no barrier among them is left waiting; what they write then is garbage, in bounds.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* ctrl) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
@@ -429,44 +484,36 @@ struct Cols {
   static constexpr int TMEM = N <= 16 ? 64 : (N <= 32 ? 128 : 256);   // S(even), S(odd), O
   static constexpr int CTAS = N <= 32 ? 2 : 1;                        // blocks an SM (shared memory)
   static __host__ __device__ int smem(int m) {
-    return kStages * (kStageV + ((m + 31) & ~31) * TT) + 4 * N * TT + (int)sizeof(AttendMisc);
+    return kVStages * kStageV + kKStages * ((m + 31) & ~31) * TT + 4 * N * TT + (int)sizeof(AttendMisc);
   }
 };
 
 template <int STR, int NH>
-__global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_kernel(PagedView c, DecodeP p, int G) {
+__global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_kernel(const __grid_constant__ CUtensorMap vmap, PagedView c, DecodeP p, int G) {
   using CC = Cols<STR, NH>;
   constexpr int N = CC::N;
   extern __shared__ __align__(1024) uint8_t dyn[];
-  const int stage_bytes = kStageV + ((c.m + 31) & ~31) * TT;
-  const int off_q = kStages * stage_bytes, off_p = off_q + 2 * N * TT;
+  const int mrows = (c.m + 31) & ~31;                         // key rows of a tile, zeros past d_store
+  const int off_k = kVStages * kStageV, off_q = off_k + kKStages * mrows * TT, off_p = off_q + 2 * N * TT;
   AttendMisc& ms = *reinterpret_cast<AttendMisc*>(dyn + off_p + 2 * N * TT);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = smem_u32(dyn);
 
-  // ---- this block's share [t0, t1) of the flat tile sequence (the lengths were written before the
-  // selection kernel started, which released this one after its own wait)
+  // ---- the tiles, and the unit that this block's first piece starts in (the lengths were written before the
+  // selection kernel started, which released this one after its own wait; so were the pages and the table)
   long long total = 0;
   for (int base = 0; base < c.B; base += kThreads) {
     const int b = base + tid;
-    int x = b < c.B ? n_tiles(seq_tokens(c, p, b)) : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    const int x = __reduce_add_sync(0xffffffffu, b < c.B ? n_tiles(seq_tokens(c, p, b)) : 0);
     __syncthreads();
     if (lane == 0) ms.scan[w] = x;
     __syncthreads();
     for (int y = 0; y < kThreads / 32; ++y) total += ms.scan[y];
   }
-  total *= c.Hkv;
-  const long long nb = min((long long)gridDim.x, total);      // every share has a tile
-  if (blockIdx.x >= nb) {
-    if (tid == 0) p.split[blockIdx.x].x = -1;
-    return;
-  }
-  const long long t0 = blockIdx.x * total / nb, t1 = (blockIdx.x + 1) * total / nb;
-  const int n_my = (int)(t1 - t0);
-  // the unit that holds tile t0
-  {
+  const Pieces pieces(total * c.Hkv, gridDim.x);
+  if (blockIdx.x >= pieces.nb && blockIdx.x > 0) return;
+  if (pieces.nb > 0) {
+    const long long t0 = pieces.start(blockIdx.x);
     long long before = 0;
     for (int base = 0; base < c.B; base += kThreads) {
       const int b = base + tid;
@@ -500,9 +547,14 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   }
   // ---- barriers, tensor memory, the columns of p that no head or part uses (zeros for good)
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&ms.full[i], kCopyThreads);
-      mbar_init(&ms.empty[i], 1);
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&ms.known[i], 1);
+      mbar_init(&ms.v_full[i], 1);
+      mbar_init(&ms.v_empty[i], 1);
+    }
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&ms.k_full[i], 2 * kKeyThreads);    // every thread's own stores, and its copies
+      mbar_init(&ms.k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.s_full[i], 1);
@@ -512,8 +564,9 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     mbar_init(&ms.drain, 1);
     fence_barrier_init();
     ms.abort = 0;
+    for (int i = 0; i < kVStages; ++i) ms.info[i] = TileInfo{0, 0, 0, 0, 0, 0, 0, 0};
   }
-  if (w == kMmaWarp) {
+  if (w == kMmaWarp && pieces.nb > 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)),
                  "r"((uint32_t)CC::TMEM)
                  : "memory");
@@ -526,54 +579,48 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  const Cursor start = ms.cur;
-  pdl_wait();                               // the selection's results; the merge of an earlier call has read its parts
-  pdl_launch_dependents();
+  if (pieces.nb == 0) {                       // no tokens at all (block 0)
+    pdl_wait();
+    if (tid == 0) p.ctl[1] = 0;
+    return;
+  }
 
-  if (w >= kCopyWarp0) {
-    // ================= copies =================
-    const int ct = tid - kCopyWarp0 * 32, lc = ct & 7, lr = ct >> 3;   // chunk and first row of every tile
-    const int pmask = (1 << c.page_log2) - 1;
-    Cursor cur = start;
-    int iu = -1, ord = -1, icount = 0, announced = 0;
-    uint2 rows = make_uint2(0, 0);
-    // page of 16 tokens of the cursor's tile, chunk `lane` (lanes 0..7 of every copy warp)
-    auto page_of_chunk = [&]() {
-      int pid = -1;
-      const int t = cur.tile * TT + 16 * lane;
-      if (lane < TT / 16 && t < cur.len) {
-        pid = __ldg(c.table + (size_t)cur.b * c.max_pages + (t >> c.page_log2));
-        if (pid < 0 || pid >= c.n_pages) {
-          pid = -1;
-          report_arg(c);
-        }
+  // page of 16 tokens of a tile, chunk `lane` (lanes 0..7 of a copying warp)
+  auto page_of_chunk = [&](int b, int tile, int len) {
+    int pid = -1;
+    const int t = tile * TT + 16 * lane;
+    if (lane < TT / 16 && t < len) {
+      pid = __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2));
+      if (pid < 0 || pid >= c.n_pages) {
+        pid = -1;
+        report_arg(c);
       }
-      return pid;
-    };
-    // tiles up to `to` have landed: tell the product warp
-    auto announce = [&](int to) {
-      fence_proxy_async_smem();
-      for (; announced <= to; ++announced) mbar_arrive(&ms.full[announced % kStages]);
-    };
-    int mypid = page_of_chunk();
-    for (int t = 0; t < n_my; ++t) {
-      const int st = t % kStages;
-      if (t >= kStages) wait_or_abort(&ms.empty[st], ((t / kStages) - 1) & 1, &ms.abort, p.ctrl);
-      const uint32_t vbase = smem0 + st * stage_bytes, kbase = vbase + kStageV;
-      const int tb = cur.tile * TT;
-      // values: rows lr, lr + 16, ..., 16 dims each; rows past the length are zeros
+    }
+    return pid;
+  };
+  const int pmask = (1 << c.page_log2) - 1;
+
+  if (w >= kKeyWarp0) {
+    // ================= key rows, scales, queries =================
+    const int ct = tid - kKeyWarp0 * 32, lc = ct & 7, lr = ct >> 3;    // chunk of 16 tokens, first row (dim)
+    auto copy_keys = [&](int t, const TileInfo& ti, int mypid, const uint4& um) {
+      const uint32_t kbase = smem0 + off_k + (t % kKStages) * mrows * TT;
+      const int pid = __shfl_sync(0xffffffffu, mypid, lc);
+      // rows lr, lr + 16, ...; rows that are not wanted are zeros
+      const uint8_t* kb = c.k;
+      if (pid >= 0) kb += c.kblock(pid, ti.g) + ((ti.tile * TT + 16 * lc) & pmask) + ((size_t)lr << c.page_log2);
+      const uint32_t words[4] = {um.x >> lr, um.y >> lr, um.z >> lr, um.w >> lr};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        if (16 * i >= mrows) break;
         const int r = lr + 16 * i;
-        const int pid = __shfl_sync(0xffffffffu, mypid, i);
-        const bool in = pid >= 0 && tb + r < cur.len;
-        const uint8_t* src = in ? c.v + c.vblock(pid, cur.g) + (size_t)((tb + r) & pmask) * D + lc * 16 : c.v;
-        cp_async16_zfill(vbase + r * D + ((lc ^ (r & 7)) << 4), src, in);
+        const bool in = pid >= 0 && ((words[i >> 1] >> (16 * (i & 1))) & 1u);
+        cp_async16_zfill(kbase + r * TT + ((lc ^ (r & 7)) << 4), kb + (in ? (size_t)(16 * i) << c.page_log2 : 0), in);
       }
-      const int pid = __shfl_sync(0xffffffffu, mypid, lc);
       if (ct < TT / 16) {                     // scales of the tile's pages; lc == ct here
+        const int st = t % kVStages;
         if (pid >= 0) {
-          const size_t si = (size_t)pid * c.Hkv + cur.g;
+          const size_t si = (size_t)pid * c.Hkv + ti.g;
           cp_async_small<4>(&ms.ks[st][ct], c.ks + si);
           cp_async_small<4>(&ms.vs[st][ct], c.vs + si);
         } else {
@@ -581,97 +628,214 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           ms.vs[st][ct] = 1.f;
         }
       }
-      if (cur.u != iu) {
+    };
+    auto finish = [&](int t, const TileInfo& ti) {
+      if (ti.flags & kFirst) {
+        // two tiles ago the buffer's last unit was done with its scores: so this tile's key buffer could be free
+        const uint32_t qbase = smem0 + off_q + ti.q * N * TT;
+        for (int i = ct; i < N * 8; i += kKeyThreads) {
+          const int r = i >> 3, ch = i & 7;
+          cp_async16_zfill(qbase + r * D + ((ch ^ (r & 7)) << 4), p.qpart + ((size_t)ti.u * N + r) * D + ch * 16, true);
+        }
+      }
+      // the copies arrive when they have landed; the product warp makes them visible to the tensor cores
+      cp_async_arrive_noinc(&ms.k_full[t % kKStages]);
+      mbar_arrive(&ms.k_full[t % kKStages]);
+    };
+    auto info_of = [&](int t) {
+      wait_or_abort(&ms.known[t % kVStages], (t / kVStages) & 1, &ms.abort, p.ctrl);
+      __syncwarp();
+      return ms.info[t % kVStages];
+    };
+    // the first tiles, while the selection runs: all their key rows
+    const uint32_t f = 0xffffffffu;
+    auto low = [&](int wd) { return c.m >= 32 * wd + 32 ? f : (c.m > 32 * wd ? (1u << (c.m - 32 * wd)) - 1u : 0u); };
+    const uint4 all = make_uint4(low(0), low(1), low(2), low(3));
+    TileInfo ti = info_of(0);
+    int mypid = page_of_chunk(ti.b, ti.tile, ti.len);
+    copy_keys(0, ti, mypid, all);
+    const bool two = !(ti.flags & kEnd);
+    TileInfo tn = ti;
+    if (two) {
+      tn = info_of(1);
+      mypid = page_of_chunk(tn.b, tn.tile, tn.len);
+      copy_keys(1, tn, mypid, all);
+    }
+    pdl_wait();                               // the selection's results
+    finish(0, ti);
+    if (two) finish(1, tn);
+    int iu = -1;
+    uint4 um = all;
+    for (int t = 2; two && !(tn.flags & kEnd); ++t) {
+      tn = info_of(t);
+      if (__any_sync(0xffffffffu, *(volatile int*)&ms.abort)) break;      // (no barrier among these warps)
+      mypid = page_of_chunk(tn.b, tn.tile, tn.len);
+      if (tn.u != iu) {
+        iu = tn.u;
+        um = p.umask[iu];
+      }
+      wait_or_abort(&ms.k_empty[t % kKStages], ((t / kKStages) - 1) & 1, &ms.abort, p.ctrl);
+      __syncwarp();
+      copy_keys(t, tn, mypid, um);
+      finish(t, tn);
+    }
+    cp_async_wait_all();
+  } else if (w == kValWarp) {
+    // ================= pieces, value rows =================
+    if (lane == 0) prefetch_tmap(&vmap);
+    Cursor cur = ms.cur;
+    int piece = blockIdx.x;
+    long long begin = pieces.start(piece), stop_at = pieces.start(piece + 1);   // the piece's tiles
+    int left = (int)(stop_at - begin);
+    const bool more = pieces.first > 0;        // there are later pieces to take
+    int iu = -1, ord = -1;
+    bool part_first = true, waited = false;    // the piece's first tile is next; the earlier kernels' results may be read
+    int seg_first = 0;                         // first tile of the unit in this piece
+    // where a piece lies among the units it shares with others, for the merge
+    auto note_split = [&]() {
+      int4 sp = make_int4(-1, 0, 0, 0);
+      if (cur.tile > 0) {
+        const long long f = begin - cur.tile;                 // the unit's tiles are [f, f + n)
+        const int first = pieces.of(f);
+        sp = make_int4(cur.u, first, pieces.of(f + n_tiles(cur.len) - 1), pieces.start(first) < f ? 1 : 0);
+      }
+      p.split[piece] = sp;
+    };
+    // The first value rows come while the selection runs; then its results, and the merge of an earlier call, which
+    // has read its parts.
+    auto after_wait = [&]() {
+      waited = true;
+      pdl_wait();
+      pdl_launch_dependents();
+      if (lane == 0) {
+        if (blockIdx.x == 0) p.ctl[1] = pieces.count();
+        const Cursor now = cur;
+        cur = ms.cur;                          // the first piece's start
+        note_split();
+        cur = now;
+      }
+    };
+    int next_piece = -1;
+    int mypid = page_of_chunk(cur.b, cur.tile, cur.len);
+    for (int t = 0;; ++t) {
+      const int st = t % kVStages;
+      if (!waited && (t >= kVStages || (more && left <= 3))) after_wait();
+      if (t >= kVStages) wait_or_abort(&ms.v_empty[st], ((t / kVStages) - 1) & 1, &ms.abort, p.ctrl);
+      __syncwarp();
+      // the piece after this one: asked for a few tiles before the end, needed at the last tile
+      if (left == 3 || (part_first && left < 3)) {
+        next_piece = -1;
+        if (lane == 0 && more && !*(volatile int*)&ms.abort) next_piece = (int)pieces.nb + atomicAdd(p.ctl, 1);
+      }
+      if (left == 1) {
+        next_piece = __shfl_sync(0xffffffffu, next_piece, 0);
+        if (next_piece >= pieces.count()) next_piece = -1;
+      }
+      const bool change = cur.u != iu || part_first, end = left == 1 && next_piece < 0;
+      if (change) {
         iu = cur.u;
         ++ord;
-        rows = *reinterpret_cast<const uint2*>(p.ulist + (size_t)iu * D + lr * 8);
-        icount = p.ucount[iu];
-        if (ord >= 2) {
-          // the buffer of unit ord - 2 is free once the products of tile t - 2 are done; they wait for tile
-          // t - 1 to be announced
-          cp_async_wait<0>();                 // committed copies: up to tile t - 1
-          announce(t - 1);
-          wait_or_abort(&ms.empty[(t - 2) % kStages], ((t - 2) / kStages) & 1, &ms.abort, p.ctrl);
-        }
-        const uint32_t qbase = smem0 + off_q + (ord & 1) * N * TT;
-        for (int i = ct; i < N * 8; i += kCopyThreads) {
-          const int r = i >> 3, ch = i & 7;
-          cp_async16_zfill(qbase + r * D + ((ch ^ (r & 7)) << 4), p.qpart + ((size_t)iu * N + r) * D + ch * 16, true);
-        }
+        part_first = false;
+        seg_first = cur.tile;
       }
-      // kept key rows lr, lr + 16, ..., chunk lc of 16 tokens; rows past the union up to the next
-      // multiple of 32 are zeros
-      const uint8_t* kb = c.k;
-      if (pid >= 0) kb += c.kblock(pid, cur.g) + ((tb + 16 * lc) & pmask);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = lr + 16 * i;
-        if (16 * i >= ((icount + 31) & ~31)) break;
-        const int d = (i < 4 ? rows.x >> (8 * i) : rows.y >> (8 * (i - 4))) & 0xff;
-        const bool in = pid >= 0 && r < icount;
-        cp_async16_zfill(kbase + r * TT + ((lc ^ (r & 7)) << 4), kb + (in ? (size_t)d << c.page_log2 : 0), in);
+      if (lane == 0) {
+        const bool unit_end = cur.tile + 1 == n_tiles(cur.len);
+        TileInfo ti;
+        ti.b = cur.b; ti.g = cur.g; ti.u = cur.u; ti.len = cur.len; ti.tile = cur.tile;
+        // a part that does not start the piece is its second
+        ti.slot = unit_end && seg_first == 0 ? -1 : 2 * piece + (begin + (cur.tile - seg_first) < stop_at - left ? 1 : 0);
+        ti.q = ord & 1;
+        ti.flags = (change ? kFirst : 0) | (unit_end || left == 1 ? kLast : 0) | (end ? kEnd : 0);
+        ms.info[st] = ti;
+        mbar_arrive(&ms.known[st]);
       }
-      cp_async_commit();
-      if (t + 1 < n_my) {
+      // one copy for each page with tokens (rows of the tile past the length, or without a page, hold what they
+      // held; the softmax threads zero them)
+      const bool go = mypid >= 0 && ((cur.tile * TT + 16 * lane) & pmask) == 0;
+      const uint32_t n_go = __popc(__ballot_sync(0xffffffffu, go));
+      if (lane == 0) mbar_arrive_expect_tx(&ms.v_full[st], n_go * (uint32_t)(D << c.page_log2));
+      __syncwarp();
+      if (go)
+        tma_rows(smem0 + st * kStageV + 16 * lane * D, &vmap, (mypid * c.Hkv + cur.g) << c.page_log2, &ms.v_full[st]);
+      if (end) break;
+      if (--left > 0) {
         next_tile(c, p, cur);
-        mypid = page_of_chunk();
+      } else {
+        // the first tile of the next piece: its sequence by the tiles before each one, 32 probes at a time
+        piece = next_piece;
+        begin = pieces.start(piece);
+        stop_at = pieces.start(piece + 1);
+        left = (int)(stop_at - begin);
+        const int want = (int)(begin / c.Hkv);
+        int lo = 0, hi = c.B;                  // prefix[lo] <= want < prefix[hi]
+        while (hi - lo > 1) {
+          const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+          const bool under = at < hi && __ldcg(p.prefix + at) <= want;
+          const int k = 31 - __clz(__ballot_sync(0xffffffffu, under));     // lane 0 is always under
+          hi = min(hi, lo + (k + 1) * step);
+          lo += k * step;
+        }
+        // sequences without tiles share their prefix with the next one: lo is the last of them, which has tiles
+        cur.b = lo;
+        cur.len = seq_tokens(c, p, lo);
+        const int x = n_tiles(cur.len), r = (int)(begin - (long long)__ldcg(p.prefix + lo) * c.Hkv);
+        cur.g = r / x;
+        cur.tile = r % x;
+        cur.u = lo * c.Hkv + cur.g;
+        part_first = true;
+        if (lane == 0) note_split();
       }
-      if (t > 0 && announced < t) {
-        cp_async_wait<1>();
-        announce(t - 1);
-      }
+      mypid = page_of_chunk(cur.b, cur.tile, cur.len);
     }
-    cp_async_wait<0>();
-    announce(n_my - 1);
+    if (!waited) after_wait();
   } else if (w == kMmaWarp) {
     // ================= products =================
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3(N);
-      Cursor cur = start;                     // tile whose scores are issued next
-      int iu = -1, ord = -1, nk = 0;
-      uint32_t firsts = 0;                    // bit t & 31: tile t is the first of its segment
+      uint32_t firsts = 0;                    // bit t & 31: tile t is the first of its part
+      int n_all = 0x7fffffff;                 // tiles, once known
       bool ok = true;
       auto issue_s = [&](int t) {
-        firsts &= ~(1u << (t & 31));
-        if (cur.u != iu) {
-          iu = cur.u;
-          ++ord;
-          nk = (p.ucount[iu] + 31) >> 5;
-          firsts |= 1u << (t & 31);
-        }
+        const int fl = ms.info[t % kVStages].flags;
+        firsts = (firsts & ~(1u << (t & 31))) | ((fl & kFirst ? 1u : 0u) << (t & 31));
+        if (fl & kEnd) n_all = t + 1;
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes + kStageV);
-        const uint64_t bd = smem_desc(smem0 + off_q + (ord & 1) * N * TT);
-        for (int k = 0; k < nk; ++k)          // 32 dims: 32 rows of A, 32 bytes of B's rows
-          tc_mma_f8(tmem + (t & 1) * N, ad + k * (32 * TT >> 4), bd + k * 2, idesc, k > 0);
+        const uint64_t ad = smem_desc(smem0 + off_k + (t % kKStages) * mrows * TT);
+        const uint64_t bd = smem_desc(smem0 + off_q + ms.info[t % kVStages].q * N * TT);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)      // 32 dims: 32 rows of A, 32 bytes of B's rows
+          if (32 * k < mrows) tc_mma_f8(tmem + (t & 1) * N, ad + k * (32 * TT >> 4), bd + k * 2, idesc, k > 0);
         tc_commit(&ms.s_full[t & 1]);
-        if (t + 1 < n_my) next_tile(c, p, cur);
+        tc_commit(&ms.k_empty[t % kKStages]);
       };
       // Whatever is ready first: the scores of tile t + 1 (its copies landed; its buffer was read before p(t - 1)
       // was announced) or the values of tile t (p written).  In a fixed order either one would hold up the other.
       int scored = 0;                         // tiles whose scores are issued
-      for (int t = 0; t < n_my; ++t) {
+      for (int t = 0; ok && t < n_all; ++t) {
         unsigned long long since = 0;
         while (true) {
-          if (scored < n_my && scored <= t + 1 && mbar_test(&ms.full[scored % kStages], (scored / kStages) & 1))
+          if (scored < n_all && scored <= t + 1 && mbar_test(&ms.k_full[scored % kKStages], (scored / kKStages) & 1))
             issue_s(scored++);
-          if (scored > t && mbar_test(&ms.p_full[t & 1], (t >> 1) & 1)) break;
+          if (scored > t && mbar_test(&ms.p_full[t & 1], (t >> 1) & 1) &&
+              mbar_test(&ms.v_full[t % kVStages], (t / kVStages) & 1))
+            break;
           if (poll_abort(&ms.abort, since, p.ctrl)) {
             ok = false;
             break;
           }
         }
         if (!ok) break;
+        fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t ad = smem_desc(smem0 + (t % kStages) * stage_bytes);
+        const uint64_t ad = smem_desc(smem0 + (t % kVStages) * kStageV);
         const uint64_t bd = smem_desc(smem0 + off_p + (t & 1) * N * TT);
         const bool first = (firsts >> (t & 31)) & 1u;
 #pragma unroll
         for (int k = 0; k < TT / 32; ++k)
           tc_mma_f8(tmem + 2 * N, ad + k * (32 * D >> 4), bd + k * 2, idesc, k > 0 || !first);
         tc_commit(&ms.pv_done[t & 1]);
-        tc_commit(&ms.empty[t % kStages]);
+        tc_commit(&ms.v_empty[t % kVStages]);
       }
       tc_commit(&ms.drain);                   // nothing is in flight when tensor memory is given back
       mbar_wait_bounded(&ms.drain, 0);
@@ -679,36 +843,34 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     __syncwarp();
   } else {
     // ================= softmax: thread = token of the tile, and dim of the output =================
-    Cursor cur = start;
+    pdl_wait();
     const uint32_t lane_base = tmem + ((uint32_t)(32 * w) << 16);
     float fac[NH], ref[NH], l[NH];
-    bool fresh = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       wait_or_abort(bar, parity, &ms.abort, p.ctrl);
       __syncwarp();                           // what follows is executed by whole warps
     };
-    int seg_start = 0, seg_tiles = 0;
     // this thread's byte in row n of p: chunk (tid / 16) ^ (n % 8)
     const uint32_t pcol = (uint32_t)(tid & 15);
     const uint32_t pchunk = (uint32_t)(tid >> 4);
-    for (int t = 0; t < n_my; ++t) {
-      if (fresh) {
-        fresh = false;
-        seg_start = cur.tile;
-        seg_tiles = 0;
+    bool begun = false;                       // O holds tiles of this part
+    for (int t = 0;; ++t) {
+      const int st = t % kVStages, buf = t & 1;
+      wait(&ms.known[st], (t / kVStages) & 1);
+      const TileInfo ti = ms.info[st];
+      if (ti.flags & kFirst) {
+        begun = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          fac[h] = h < G ? p.qfac[(size_t)cur.u * kMaxG + h] : 0.f;
+          fac[h] = h < G ? p.qfac[(size_t)ti.u * kMaxG + h] : 0.f;
           ref[h] = -INFINITY;
           l[h] = 0.f;
         }
       }
-      const int st = t % kStages, buf = t & 1;
-      wait(&ms.full[st], (t / kStages) & 1);  // the scales
-      wait(&ms.s_full[buf], (t >> 1) & 1);
+      wait(&ms.s_full[buf], (t >> 1) & 1);    // and the scales have landed, before the scores were issued
       tc_fence_after();
       const float ksc = ms.ks[st][tid >> 4], vsc = ms.vs[st][tid >> 4];
-      const bool seen = ksc >= 0.f && cur.tile * TT + tid < cur.len;
+      const bool seen = ksc >= 0.f && ti.tile * TT + tid < ti.len;
       const float lv = __log2f(vsc), iv = 1.f / vsc;
       float x[NH];
       bool raise = false;
@@ -727,8 +889,10 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           raise |= h < G && x[h] > ref[h] + kLazy;
         }
       }
+      // one thread decides for all whether an abort ends the work here
+      if (tid == 0) ms.stop[buf] = *(volatile int*)&ms.abort;
       if (named_bar_or(1, kSoftThreads, raise)) {
-        // a score far above the reference (always in a unit's first tile): raise it to the tile's maximum
+        // a score far above the reference (always in a part's first tile): raise it to the tile's maximum
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           if (h >= G) break;
@@ -750,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
             l[h] *= al[h];
           }
         }
-        if (seg_tiles > 0) {
+        if (begun) {
           wait(&ms.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
           tc_fence_after();
 #pragma unroll
@@ -766,6 +930,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         }
         named_bar_sync(1, kSoftThreads);      // ms.red is free again
       }
+      if (ms.stop[buf]) break;
+      begun = true;
       if (t >= 2) wait(&ms.pv_done[buf], ((t - 2) >> 1) & 1);
       uint8_t* pb = dyn + off_p + buf * N * TT + pcol;
 #pragma unroll
@@ -788,20 +954,20 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           }
         }
       }
+      if (!seen) {
+        // a row that is not the sequence's: zeros, since 0 times what is stored there may be NaN
+        wait_or_abort(&ms.v_full[st], (t / kVStages) & 1, &ms.abort, p.ctrl);
+        uint4* row = reinterpret_cast<uint4*>(dyn + st * kStageV + tid * D);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(&ms.p_full[buf]);
-      ++seg_tiles;
+      if (!(ti.flags & kLast)) continue;
 
-      // ---- end of the unit, or of this block's share of it
-      const bool last_tile = cur.tile + 1 == n_tiles(cur.len);
-      if (!last_tile && t + 1 < n_my) {
-        ++cur.tile;
-        continue;
-      }
-      const bool whole = seg_start == 0 && last_tile;
-      const size_t row0 = (size_t)cur.b * p.Hq + (size_t)cur.g * G;
-      const int slot = 2 * blockIdx.x + (t + 1 > seg_tiles ? 1 : 0);      // 0: the share's first piece
+      // ---- end of the unit, or of this piece's share of it
+      const size_t row0 = (size_t)ti.b * p.Hq + (size_t)ti.g * G;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         if (h >= G) break;
@@ -827,33 +993,19 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           const float L = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
           // p was held times 2^kPScale, so M + log2 l is off by it
           const float M = ref[h] - kPScale;
-          if (whole) {
+          if (ti.slot < 0) {
             store_out_elem(p, (row0 + h) * D + tid, normalised(O, L));
             if (p.lse_out && tid == 0) p.lse_out[row0 + h] = lse_of(M, L);
           } else {
-            p.part_o[((size_t)slot * kMaxG + h) * D + tid] = O;
-            if (tid == 0) p.part_ml[(size_t)slot * kMaxG + h] = make_float2(M, L);
+            p.part_o[((size_t)ti.slot * G + h) * D + tid] = O;
+            if (tid == 0) p.part_ml[(size_t)ti.slot * G + h] = make_float2(M, L);
           }
         }
       }
       tc_fence_before();
       named_bar_sync(1, kSoftThreads);        // ms.red is free again
-      if (t + 1 < n_my) {
-        fresh = true;
-        next_unit(c, p, cur);
-      }
+      if (ti.flags & kEnd) break;
     }
-  }
-  // the block's place among the units it shares with others, for the merge
-  if (tid == kMmaWarp * 32 + 1) {
-    int4 sp = make_int4(-1, 0, 0, 0);
-    if (start.tile > 0) {
-      // the unit's tiles are [f, f + n) of the flat sequence; tile x lies in block ((x + 1) nb - 1) / total
-      const long long f = t0 - start.tile, n = n_tiles(start.len);
-      const long long first = ((f + 1) * nb - 1) / total, last = ((f + n) * nb - 1) / total;
-      sp = make_int4(start.u, (int)first, (int)last, first * total / nb < f ? 1 : 0);
-    }
-    p.split[blockIdx.x] = sp;
   }
   __syncthreads();
   if (w == kMmaWarp)
@@ -864,72 +1016,87 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 // merge of the parts of units that several blocks shared
 // ============================================================================
 
-// One block per (boundary between two attention blocks, query head of the group);
-// the first boundary inside a unit merges it.  Each of eight warps adds every
+// Blocks share the boundaries between pieces; the first boundary inside a unit
+// merges it, for one query head of the group.  Each of eight warps adds every
 // eighth part, a float4 of O per lane, then the eight sums are added in order.
 constexpr int kMergeWarps = 8;
 constexpr int kMaxParts = 2048;
+constexpr int kPiecesPerBlock = 4;         // one first piece and three later ones
 
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
   __shared__ float fac[kMaxParts];
   __shared__ __align__(16) float sum[kMergeWarps][D];
   __shared__ float red[2][kMergeWarps];
-  const int x = blockIdx.x + 1, hh = blockIdx.y, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int hh = blockIdx.y, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int4 sp = p.split[x];
-  if (sp.x < 0 || sp.y != x - 1) return;
-  const int n = sp.z - sp.y + 1;
-  auto slot = [&](int i) { return (size_t)(2 * (sp.y + i) + (i == 0 ? sp.w : 0)) * kMaxG + hh; };
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += kMergeWarps * 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+  const int n_pieces = p.ctl[1];
+  int4 sps[kPiecesPerBlock];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[0][w] = M;
-  __syncthreads();
-#pragma unroll
-  for (int y = 0; y < kMergeWarps; ++y) M = fmaxf(M, red[0][y]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int i = tid; i < n; i += kMergeWarps * 32) {
-    const float2 ml = p.part_ml[slot(i)];
-    const float f = fast_exp2(ml.x - ref);
-    fac[i] = f;
-    L = fmaf(ml.y, f, L);
+  for (int y = 0; y < kPiecesPerBlock; ++y) {
+    const int x = 1 + blockIdx.x + y * gridDim.x;
+    sps[y] = make_int4(-1, 0, 0, 0);
+    if (x < n_pieces) sps[y] = p.split[x];
   }
+#pragma unroll 1
+  for (int y = 0; y < kPiecesPerBlock; ++y) {
+    const int x = 1 + blockIdx.x + y * gridDim.x;
+    const int4 sp = y == 0 ? sps[0] : (y == 1 ? sps[1] : (y == 2 ? sps[2] : sps[3]));
+    if (sp.x < 0 || sp.y != x - 1) continue;
+    const int n = sp.z - sp.y + 1;
+    auto slot = [&](int i) { return (size_t)(2 * (sp.y + i) + (i == 0 ? sp.w : 0)) * G + hh; };
+    float M = -INFINITY;
+    for (int i = tid; i < n; i += kMergeWarps * 32) M = fmaxf(M, p.part_ml[slot(i)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) red[1][w] = L;
-  __syncthreads();
-  L = 0.f;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][w] = M;
+    __syncthreads();
 #pragma unroll
-  for (int y = 0; y < kMergeWarps; ++y) L += red[1][y];
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z = 0; z < kMergeWarps; ++z) M = fmaxf(M, red[0][z]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int i = tid; i < n; i += kMergeWarps * 32) {
+      const float2 ml = p.part_ml[slot(i)];
+      const float f = fast_exp2(ml.x - ref);
+      fac[i] = f;
+      L = fmaf(ml.y, f, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) red[1][w] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int z = 0; z < kMergeWarps; ++z) L += red[1][z];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = w; i < n; i += kMergeWarps) {
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * lane);
-    const float f = fac[i];
-    acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
-  }
-  *reinterpret_cast<float4*>(&sum[w][4 * lane]) = acc;
-  __syncthreads();
-  if (tid < D) {
-    float O = 0.f;
+    for (int i = w; i < n; i += kMergeWarps) {
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * lane);
+      const float f = fac[i];
+      acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+    }
+    *reinterpret_cast<float4*>(&sum[w][4 * lane]) = acc;
+    __syncthreads();
+    if (tid < D) {
+      float O = 0.f;
 #pragma unroll
-    for (int y = 0; y < kMergeWarps; ++y) O += sum[y][tid];
-    const size_t row = (size_t)(sp.x / c.Hkv) * p.Hq + (size_t)(sp.x % c.Hkv) * G + hh;
-    store_out_elem(p, row * D + tid, normalised(O, L));
-    if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(M, L);
+      for (int z = 0; z < kMergeWarps; ++z) O += sum[z][tid];
+      const size_t row = (size_t)(sp.x / c.Hkv) * p.Hq + (size_t)(sp.x % c.Hkv) * G + hh;
+      store_out_elem(p, row * D + tid, normalised(O, L));
+      if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(M, L);
+    }
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- host side
 struct Layout {
-  size_t ucount, ulist, qpart, qfac, part_ml, part_o, split, total;
+  size_t umask, qpart, qfac, prefix, ctl, part_ml, part_o, split, total;
 };
 
 // The workspace does not depend on the output type: room for the widest operands.
-Layout layout_of(int n_units, int G, int blocks) {
+Layout layout_of(int B, int Hkv, int G, int blocks) {
+  const int n_units = B * Hkv, pieces = kPiecesPerBlock * blocks;
   const int cols = G > 4 ? 64 : 32;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -938,20 +1105,21 @@ Layout layout_of(int n_units, int G, int blocks) {
     return r;
   };
   Layout y;
-  y.ucount = take((size_t)n_units * 4);
-  y.ulist = take((size_t)n_units * D);
+  y.umask = take((size_t)n_units * sizeof(uint4));
   y.qpart = take((size_t)n_units * cols * D);
   y.qfac = take((size_t)n_units * kMaxG * 4);
-  y.part_ml = take((size_t)2 * blocks * kMaxG * sizeof(float2));
-  y.part_o = take((size_t)2 * blocks * kMaxG * D * 4);
-  y.split = take((size_t)blocks * sizeof(int4));
+  y.prefix = take((size_t)(B + 1) * 4);
+  y.ctl = take(2 * 4);
+  y.part_ml = take((size_t)2 * pieces * G * sizeof(float2));
+  y.part_o = take((size_t)2 * pieces * G * D * 4);
+  y.split = take((size_t)pieces * sizeof(int4));
   y.total = at;
   return y;
 }
 
 int attend_blocks(int per_sm) {
   const int n = per_sm * device_sm_count();
-  return n < kMaxParts ? n : kMaxParts;
+  return n < kMaxParts / kPiecesPerBlock ? n : kMaxParts / kPiecesPerBlock;
 }
 
 template <typename T>
@@ -969,11 +1137,15 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   const int smem = CC::smem(c.m), blocks = attend_blocks(CC::CTAS);
   int rc = set_smem_limit(paged_attend_kernel<STR, NH>, smem, "paged_attend_kernel");
   if (rc != AQUA_OK) return rc;
+  // value pages as rows of 128 bytes (64 columns of two), a page a box
+  CUtensorMap vmap;
+  rc = encode_tmap_bf16_2d(&vmap, c.v, D / 2, (uint64_t)c.n_pages * c.Hkv << c.page_log2, D, D / 2, c.page, true);
+  if (rc != AQUA_OK) return rc;
   cudaError_t e = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NH, STR, CC::QPARTS, st)
                        : launch_select<float>(c, p, G, NH, STR, CC::QPARTS, st);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
   if ((rc = check_launch("paged_select_kernel")) != AQUA_OK) return rc;
-  e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, c, p, G);
+  e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
   if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK || blocks < 2) return rc;
   e = launch_pdl(paged_merge_kernel, dim3(blocks - 1, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
@@ -983,20 +1155,21 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int n_units, int G) { return layout_of(n_units, G, attend_blocks(2)).total; }
+size_t paged_decode_workspace_bytes(int B, int Hkv, int G) { return layout_of(B, Hkv, G, attend_blocks(2)).total; }
 
 int launch_paged_decode(const PagedView& c, const int32_t* len, const void* q, bool bf16, const Strides& qs,
                         const float* P, const RopeView& rope, int Hq, int k, float scale, void* out, bool out_bf16,
                         int32_t* sel_out, float* qproj_out, float* lse_out, void* ws, cudaStream_t st) {
-  const int n_units = c.B * c.Hkv, G = Hq / c.Hkv;
-  const Layout y = layout_of(n_units, G, attend_blocks(2));
+  const int G = Hq / c.Hkv;
+  const Layout y = layout_of(c.B, c.Hkv, G, attend_blocks(2));
   uint8_t* base = static_cast<uint8_t*>(ws);
   DecodeP p;
   p.len = len; p.q = q; p.qs = qs; p.P = P; p.rope = rope; p.Hq = Hq; p.k = k; p.scale = scale;
   p.out = out; p.out_bf16 = out_bf16; p.sel_out = sel_out; p.qproj_out = qproj_out; p.lse_out = lse_out;
   p.ctrl = c.ctrl;
-  p.ucount = reinterpret_cast<int32_t*>(base + y.ucount);
-  p.ulist = base + y.ulist;
+  p.umask = reinterpret_cast<uint4*>(base + y.umask);
+  p.prefix = reinterpret_cast<int32_t*>(base + y.prefix);
+  p.ctl = reinterpret_cast<int32_t*>(base + y.ctl);
   p.qpart = base + y.qpart;
   p.qfac = reinterpret_cast<float*>(base + y.qfac);
   p.part_ml = reinterpret_cast<float2*>(base + y.part_ml);
