@@ -111,40 +111,46 @@ __device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -I
 // rotation, projection, top-k
 // ============================================================================
 
+// A chain of latencies: everything that does not need the earlier kernels' results (P, in f64) is done before
+// the wait on them, and after the projection each head is one warp's business.
 // GP: the group size padded to 1, 2, 4 or 8 (rows G .. GP-1 are zeros and never stored).
 template <typename T, int GP>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, DecodeP p, int G, int NH, int stride, int parts) {
   constexpr int kSlices = kSelThreads / D, kRows = D / kSlices;      // P rows per thread
-  __shared__ __align__(16) double qd[GP][D];       // rotated rows; later the ranking keys
+  __shared__ __align__(16) double qd[GP][D];       // rotated rows
   __shared__ double part[kSlices][GP][D];
-  __shared__ float qs[GP][D];                      // raw rows; later the kept q~, 0 elsewhere
-  float (*raw)[D] = qs;
-  uint32_t (*key)[D] = reinterpret_cast<uint32_t (*)[D]>(&qd[0][0]);
+  __shared__ float raw[GP][D];
   __shared__ uint32_t kept[GP][4];
-  __shared__ float qmul[GP];
   __shared__ int before;
   const int u = blockIdx.x, b = u / c.Hkv, g = u % c.Hkv;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int j = tid & 127, sl = tid >> 7;
   // P is read before the wait on the previous kernel: whatever may still run then does not write it
-  float pr[kRows];
+  double pr[kRows];
   {
     const float* Pg = p.P + (size_t)g * D * D + (size_t)sl * kRows * D + j;
+    float f[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) pr[i] = __ldg(Pg + i * D);
+    for (int i = 0; i < kRows; ++i) f[i] = __ldg(Pg + i * D);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      pr[i] = f[i];
+      asm volatile("" : "+d"(pr[i]));      // here, not behind the wait
+    }
   }
   pdl_wait();
   pdl_launch_dependents();
   const int len = __ldg(p.len + b);
+  const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
+  for (int i = tid; i < GP * D; i += kSelThreads)
+    raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
   bool bad;
   const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
   if (tid == 0) {
     if (bad) report_arg(c);
     if (u == 0) p.ctl[0] = 0;
+    before = 0;
   }
-  const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
-  for (int i = tid; i < GP * D; i += kSelThreads)
-    raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
   __syncthreads();
   for (int i = tid; i < GP * D; i += kSelThreads) {
     const int hh = i >> 7;
@@ -161,109 +167,123 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
     for (int hh = 0; hh < GP; ++hh) acc[hh] = 0.0;
 #pragma unroll
     for (int i = 0; i < kRows; i += 2) {
-      const double x0 = pr[i], x1 = pr[i + 1];
 #pragma unroll
       for (int hh = 0; hh < GP; ++hh) {
         const double2 qv = *reinterpret_cast<const double2*>(&qd[hh][sl * kRows + i]);
-        acc[hh] = fma(x1, qv.y, fma(x0, qv.x, acc[hh]));
+        acc[hh] = fma(pr[i + 1], qv.y, fma(pr[i], qv.x, acc[hh]));
       }
     }
 #pragma unroll
     for (int hh = 0; hh < GP; ++hh) part[sl][hh][j] = acc[hh];
   }
   __syncthreads();
-  for (int i = tid; i < GP * D; i += kSelThreads) {
-    const int hh = i >> 7;
-    double sum = part[0][hh][j];
+  if (w < G) {
+    // ---- head w: lane holds dims lane + 32 y
+    float qt[4];
+    uint32_t key[4];
 #pragma unroll
-    for (int x = 1; x < kSlices; ++x) sum += part[x][hh][j];
-    const float qt = (float)sum;
-    qs[hh][j] = qt;
-    // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
-    key[hh][j] = j < c.m ? min(__float_as_uint(fabsf(qt)), 0x7F800001u) + 1u : 0u;
-    if (p.qproj_out && hh < G) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G) * D + i] = qt;
-  }
-  __syncthreads();
-  // Dimension j is kept when fewer than k others rank before it (larger, or equal and lower).  Four
-  // warps a head count the larger ones; equal keys are looked at only if they straddle the cut.
-  for (int hh = sl; hh < G; hh += kSlices) {
-    const uint32_t kj = key[hh][j];
-    int rank = 0;
-#pragma unroll 8
-    for (int x = 0; x < D; x += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&key[hh][x]);
-      rank += (int)(o.x > kj) + (int)(o.y > kj) + (int)(o.z > kj) + (int)(o.w > kj);
+    for (int y = 0; y < 4; ++y) {
+      const int i = lane + 32 * y;
+      double sum = part[0][w][i];
+#pragma unroll
+      for (int x = 1; x < kSlices; ++x) sum += part[x][w][i];
+      qt[y] = (float)sum;
+      // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
+      key[y] = i < c.m ? min(__float_as_uint(fabsf(qt[y])), 0x7F800001u) + 1u : 0u;
+      if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G + w) * D + i] = qt[y];
     }
-    const int in = named_bar_popc(2 + sl, D, j < c.m && rank < p.k);
-    if (in > p.k) {
-      for (int x = 0; x < j; ++x) rank += key[hh][x] == kj;
-    }
-    const uint32_t bal = __ballot_sync(0xffffffffu, j < c.m && rank < p.k);
-    if (lane == 0) kept[hh][w & 3] = bal;
-  }
-  __syncthreads();
-  // masked rows, their selected dims, and each head's power-of-two normaliser
-  for (int i = tid; i < G * D; i += kSelThreads) {
-    const int hh = i >> 7, wd = j >> 5;
-    const uint32_t word = kept[hh][wd];
-    if ((word >> (j & 31)) & 1u) {
-      if (p.sel_out) {
-        int pos = __popc(word & ((1u << (j & 31)) - 1u));
-        for (int x = 0; x < wd; ++x) pos += __popc(kept[hh][x]);
-        p.sel_out[((size_t)b * p.Hq + (size_t)g * G + hh) * p.k + pos] = j;
+    // tau: the largest value with at least k keys >= tau, a bit a round from the top; the search ends when
+    // exactly k are
+    uint32_t tau = 0;
+    int cnt = D;
+#pragma unroll 1
+    for (int bit = 30; bit >= 0 && cnt != p.k; --bit) {
+      const uint32_t cand = tau | (1u << bit);
+      const int n_ge = __reduce_add_sync(0xffffffffu, (int)(key[0] >= cand) + (int)(key[1] >= cand) + (int)(key[2] >= cand) +
+                                                          (int)(key[3] >= cand));
+      if (n_ge >= p.k) {
+        tau = cand;
+        cnt = n_ge;
       }
-    } else {
-      qs[hh][j] = 0.f;
+    }
+    uint32_t word[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) word[y] = __ballot_sync(0xffffffffu, key[y] >= tau && key[y] > 0);
+    if (cnt != p.k) {
+      // equal keys straddle the cut: every key above tau, then keys equal to tau from the lowest dim up
+      int need = p.k;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) need -= __popc(__ballot_sync(0xffffffffu, key[y] > tau));
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t eq = __ballot_sync(0xffffffffu, key[y] == tau && key[y] > 0);
+        const bool take = key[y] > tau || (key[y] == tau && key[y] > 0 && __popc(eq & ((1u << lane) - 1u)) < need);
+        need -= min(need, __popc(eq));
+        word[y] = __ballot_sync(0xffffffffu, take);
+      }
+    }
+    float mx = 0.f;
+    int pos = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const bool keep = (word[y] >> lane) & 1u;
+      if (keep) {
+        if (p.sel_out)
+          p.sel_out[((size_t)b * p.Hq + (size_t)g * G + w) * p.k + pos + __popc(word[y] & ((1u << lane) - 1u))] = lane + 32 * y;
+        mx = fmaxf(mx, finite_abs(qt[y]));
+      } else {
+        qt[y] = 0.f;
+      }
+      pos += __popc(word[y]);
+      if (lane == 0) kept[w][y] = word[y];
+    }
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
+    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+    const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+    if (lane == 0) p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
+    // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
+    // most half a step, so 16 times it stays in range)
+    uint8_t* dst = p.qpart + ((size_t)u * NH + w) * stride * D + lane;
+#pragma unroll
+    for (int y = 0; y < 4; y += 2) {
+      float x0 = qt[y] * mul, x1 = qt[y + 1] * mul;
+      if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // an infinite query makes its scores NaN, not the largest code
+      if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+      for (int i = 0; i < stride; ++i) {
+        const uint16_t code = i < parts ? f32x2_to_e4m3x2(x0, x1) : (uint16_t)0;
+        dst[i * D + 32 * y] = (uint8_t)code;
+        dst[i * D + 32 * y + 32] = (uint8_t)(code >> 8);
+        const float2 back = e4m3x2_to_f32x2(code);
+        x0 = (x0 - back.x) * 16.f;
+        x1 = (x1 - back.y) * 16.f;
+      }
+    }
+  } else if (w >= 8) {
+    // zeros for the heads the operand has room for but the group lacks
+    for (int i = tid - 256; i < (NH - G) * stride * (D / 16); i += kSelThreads - 256)
+      reinterpret_cast<uint4*>(p.qpart + ((size_t)u * NH + G) * stride * D)[i] = make_uint4(0, 0, 0, 0);
+    // tiles of the sequences before this one (one block of each sequence)
+    if (g == 0) {
+      int sum = 0;
+      for (int x = tid - 256; x < b; x += kSelThreads - 256) sum += n_tiles(seq_tokens(c, p, x));
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0 && sum != 0) atomicAdd(&before, sum);
     }
   }
+  __syncthreads();
   if (tid == 0) {
     uint4 um = make_uint4(0, 0, 0, 0);
-    for (int hh = 0; hh < G; ++hh) {
+#pragma unroll
+    for (int hh = 0; hh < GP; ++hh) {
+      if (hh >= G) break;
       um.x |= kept[hh][0];
       um.y |= kept[hh][1];
       um.z |= kept[hh][2];
       um.w |= kept[hh][3];
     }
     p.umask[u] = um;
-  }
-  __syncthreads();
-  if (w < G) {
-    float mx = 0.f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) mx = fmaxf(mx, finite_abs(qs[w][lane + 32 * x]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
-    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-    if (lane == 0) {
-      qmul[w] = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
-    }
-  }
-  __syncthreads();
-  // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
-  // most half a step, so 16 times it stays in range)
-  for (int i = tid; i < NH * D; i += kSelThreads) {
-    const int hh = i >> 7;
-    float x = hh < G ? qs[hh][j] * qmul[hh] : 0.f;
-    if (!(fabsf(x) < INFINITY)) x = NAN;      // an infinite query makes its scores NaN, not the largest code
-    uint8_t* dst = p.qpart + ((size_t)u * NH + hh) * stride * D + j;
-    for (int y = 0; y < stride; ++y) {
-      const uint16_t code = y < parts ? f32x2_to_e4m3x2(x, 0.f) : (uint16_t)0;
-      dst[y * D] = (uint8_t)code;
-      x = (x - e4m3x2_to_f32x2(code).x) * 16.f;
-    }
-  }
-  // tiles of the sequences before this one (one block of each sequence)
-  if (g == 0) {
-    if (tid == 0) before = 0;
-    __syncthreads();
-    int sum = 0;
-    for (int x = tid; x < b; x += kSelThreads) sum += n_tiles(seq_tokens(c, p, x));
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0 && sum != 0) atomicAdd(&before, sum);
-    __syncthreads();
-    if (tid == 0) {
+    if (g == 0) {
       p.prefix[b] = before;
       if (b == c.B - 1) p.prefix[c.B] = before + n_tiles(n);
     }
@@ -295,8 +315,8 @@ struct Pieces {
   long long total, nb;
   long long first, rest;   // tiles of a first piece and of a later one; first = 0: equal shares, nothing else
   __device__ __forceinline__ Pieces(long long t, int blocks) : total(t), nb(min((long long)blocks, t)), first(0), rest(1) {
-    // worth it from eight tiles a block on: three later pieces each
-    if (nb > 0 && total >= 8 * nb) {
+    // worth it from five tiles a block on: three later pieces each
+    if (nb > 0 && total >= 5 * nb) {
       first = total * 5 / 8 / nb;
       const long long left = total - first * nb;
       rest = (left + 3 * nb - 1) / (3 * nb);
@@ -1017,73 +1037,79 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 // ============================================================================
 
 // Blocks share the boundaries between pieces; the first boundary inside a unit
-// merges it, for one query head of the group.  Each of eight warps adds every
-// eighth part, a float4 of O per lane, then the eight sums are added in order.
+// merges it, for one query head of the group.  Bound by the latency of two dependent
+// loads: which parts, and the parts (M, l and O together, eight at a time).  Each of eight warps
+// runs over every eighth part, a float4 of O per lane; then the eight results are
+// added in order.
 constexpr int kMergeWarps = 8;
-constexpr int kMaxParts = 2048;
+constexpr int kMaxPieces = 2048;
 constexpr int kPiecesPerBlock = 4;         // one first piece and three later ones
 
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
-  __shared__ float fac[kMaxParts];
   __shared__ __align__(16) float sum[kMergeWarps][D];
-  __shared__ float red[2][kMergeWarps];
+  __shared__ float2 ml[kMergeWarps];
   const int hh = blockIdx.y, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_wait();
   const int n_pieces = p.ctl[1];
-  int4 sps[kPiecesPerBlock];
+  int4 sps[kPiecesPerBlock];               // fetched along with their number: the array has room for every one asked for
+#pragma unroll
+  for (int y = 0; y < kPiecesPerBlock; ++y) sps[y] = p.split[min(1 + (int)(blockIdx.x + y * gridDim.x), kPiecesPerBlock * (int)gridDim.x - 1)];
 #pragma unroll
   for (int y = 0; y < kPiecesPerBlock; ++y) {
     const int x = 1 + blockIdx.x + y * gridDim.x;
-    sps[y] = make_int4(-1, 0, 0, 0);
-    if (x < n_pieces) sps[y] = p.split[x];
-  }
-#pragma unroll 1
-  for (int y = 0; y < kPiecesPerBlock; ++y) {
-    const int x = 1 + blockIdx.x + y * gridDim.x;
-    const int4 sp = y == 0 ? sps[0] : (y == 1 ? sps[1] : (y == 2 ? sps[2] : sps[3]));
-    if (sp.x < 0 || sp.y != x - 1) continue;
+    const int4 sp = sps[y];
+    if (x >= n_pieces || sp.x < 0 || sp.y != x - 1) continue;
     const int n = sp.z - sp.y + 1;
-    auto slot = [&](int i) { return (size_t)(2 * (sp.y + i) + (i == 0 ? sp.w : 0)) * G + hh; };
-    float M = -INFINITY;
-    for (int i = tid; i < n; i += kMergeWarps * 32) M = fmaxf(M, p.part_ml[slot(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][w] = M;
-    __syncthreads();
-#pragma unroll
-    for (int z = 0; z < kMergeWarps; ++z) M = fmaxf(M, red[0][z]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int i = tid; i < n; i += kMergeWarps * 32) {
-      const float2 ml = p.part_ml[slot(i)];
-      const float f = fast_exp2(ml.x - ref);
-      fac[i] = f;
-      L = fmaf(ml.y, f, L);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) red[1][w] = L;
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int z = 0; z < kMergeWarps; ++z) L += red[1][z];
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = w; i < n; i += kMergeWarps) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + 4 * lane);
-      const float f = fac[i];
-      acc.x = fmaf(v.x, f, acc.x); acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z); acc.w = fmaf(v.w, f, acc.w);
+#pragma unroll 1
+    for (int i0 = w; i0 < n; i0 += 8 * kMergeWarps) {
+      float2 m[8];
+      float4 v[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const int i = i0 + z * kMergeWarps;
+        m[z] = make_float2(-INFINITY, 0.f);
+        v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const size_t slot = (size_t)(2 * (sp.y + i) + (i == 0 ? sp.w : 0)) * G + hh;
+          m[z] = p.part_ml[slot];
+          v[z] = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * lane);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) top = fmaxf(top, m[z].x);
+      const float ref = top == -INFINITY ? 0.f : top, al = fast_exp2(M - ref);
+      M = top;
+      L *= al;
+      acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const float f = fast_exp2(m[z].x - ref);
+        L = fmaf(m[z].y, f, L);
+        acc.x = fmaf(v[z].x, f, acc.x); acc.y = fmaf(v[z].y, f, acc.y);
+        acc.z = fmaf(v[z].z, f, acc.z); acc.w = fmaf(v[z].w, f, acc.w);
+      }
     }
     *reinterpret_cast<float4*>(&sum[w][4 * lane]) = acc;
+    if (lane == 0) ml[w] = make_float2(M, L);
     __syncthreads();
     if (tid < D) {
-      float O = 0.f;
+      float top = -INFINITY;
 #pragma unroll
-      for (int z = 0; z < kMergeWarps; ++z) O += sum[z][tid];
+      for (int z = 0; z < kMergeWarps; ++z) top = fmaxf(top, ml[z].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float O = 0.f, Ls = 0.f;
+#pragma unroll
+      for (int z = 0; z < kMergeWarps; ++z) {
+        const float f = fast_exp2(ml[z].x - ref);
+        O = fmaf(sum[z][tid], f, O);
+        Ls = fmaf(ml[z].y, f, Ls);
+      }
       const size_t row = (size_t)(sp.x / c.Hkv) * p.Hq + (size_t)(sp.x % c.Hkv) * G + hh;
-      store_out_elem(p, row * D + tid, normalised(O, L));
-      if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(M, L);
+      store_out_elem(p, row * D + tid, normalised(O, Ls));
+      if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(top, Ls);
     }
     __syncthreads();
   }
@@ -1119,7 +1145,7 @@ Layout layout_of(int B, int Hkv, int G, int blocks) {
 
 int attend_blocks(int per_sm) {
   const int n = per_sm * device_sm_count();
-  return n < kMaxParts / kPiecesPerBlock ? n : kMaxParts / kPiecesPerBlock;
+  return n < kMaxPieces / kPiecesPerBlock ? n : kMaxPieces / kPiecesPerBlock;
 }
 
 template <typename T>
@@ -1147,8 +1173,9 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   if ((rc = check_launch("paged_select_kernel")) != AQUA_OK) return rc;
   e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
-  if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK || blocks < 2) return rc;
-  e = launch_pdl(paged_merge_kernel, dim3(blocks - 1, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
+  if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK) return rc;
+  // 4 * blocks boundaries, which is as many as there are pieces
+  e = launch_pdl(paged_merge_kernel, dim3(blocks, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
   return check_launch("paged_merge_kernel");
 }

@@ -477,6 +477,66 @@ def test_decode_many_sequences():
     check_decode(got, ref, lens, k, m, False)
 
 
+def torch_decode(cache, q, lens, P, k):
+    """The step in f64 on the device, for lengths the loops of the oracle are too slow for (no rotation)."""
+    B, Hq, _ = q.shape
+    H, m, G = cache.Hkv, cache.d_store, Hq // cache.Hkv
+    out = torch.zeros(B, Hq, 128, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        t = cache.block_table[b, :-(-n // cache.page_size)].long()
+        kk = cache.k_pages[t].view(torch.float8_e4m3fn).double() * cache.k_scale[t].double()[:, :, None, None]
+        vv = cache.v_pages[t].view(torch.float8_e4m3fn).double() * cache.v_scale[t].double()[:, :, None, None]
+        kk, vv = kk.permute(1, 2, 0, 3).reshape(H, m, -1)[..., :n], vv.permute(1, 0, 2, 3).reshape(H, -1, 128)[:, :n]
+        for h in range(H):
+            qt = q[b, h * G:(h + 1) * G].double() @ P[h].double()
+            keep = qt[:, :m].abs().topk(k, dim=1).indices
+            qm = torch.zeros(G, m, dtype=torch.float64, device="cuda").scatter_(1, keep, qt.gather(1, keep))
+            out[b, h * G:(h + 1) * G] = torch.softmax(qm @ kk[h] / 128 ** 0.5, -1) @ vv[h]
+    return out
+
+
+@pytest.mark.parametrize("tiles", [7.99, 8, 8.01, 16, 37.3, 5, 4.99])
+def test_decode_long_sequence_in_many_pieces(tiles):
+    """One sequence split over all blocks: equal shares, the most later pieces there can be, fewer of them."""
+    blocks = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    n = int(blocks * tiles) * 128 - 5
+    rng = np.random.default_rng(40)
+    _, P32 = calib_P(1)
+    cache = make_cache(1, 1, 128, 32, -(-n // 128), seed=41)
+    q = tdev(rows_of(rng, 1, 4, "f32", 0.3))
+    for od, tol in ((torch.float32, 1e-5), (torch.bfloat16, 4e-3)):         # bf16: against the unrounded result
+        out = torch.empty(1, 4, 128, dtype=od, device="cuda")
+        ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, 4),), 0xFF, dtype=torch.uint8, device="cuda")
+        aq.aqua_paged_decode_attn(cache.desc, q, torch.tensor([n], dtype=torch.int32, device="cuda"), tdev(P32), 4, 20, out, ws)
+        ref = torch_decode(cache, q, [n], tdev(P32), 20)
+        assert float(((out.double() - ref).norm(dim=-1) / ref.norm(dim=-1)).max()) <= tol
+
+
+def test_decode_ragged_long_batch():
+    """Units that end inside pieces of every kind, the same bits on every run."""
+    rng = np.random.default_rng(42)
+    B, Hq, Hkv, m, k = 24, 16, 8, 96, 64
+    lens = [int(x) for x in np.exp(rng.uniform(0, np.log(12000), B))]
+    lens[3], lens[11] = 0, 12000
+    _, P32 = calib_P(Hkv)
+    P = tdev(P32)
+    cache = make_cache(B, Hkv, 64, m, 12000 // 64 + 1, seed=43)
+    q = tdev(rows_of(rng, B, Hq, "f32", 0.3))
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, Hq),), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(6):
+        out = torch.empty(B, Hq, 128, device="cuda")
+        aq.aqua_paged_decode_attn(cache.desc, q, lt, P, Hq, k, out, ws)
+        outs.append(out)
+    ref = torch_decode(cache, q, lens, P, k)
+    live = lt > 0
+    assert float(((outs[0].double() - ref).norm(dim=-1)[live] / ref.norm(dim=-1)[live]).max()) <= 1e-5
+    assert bool((outs[0][3] == 0).all())
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 def test_decode_ties_and_zero_queries():
     """Equal magnitudes go to the lower dimension; a zero query keeps the first k and attends evenly."""
     B, Hq, Hkv, page, m, k, lens = 2, 4, 1, 16, 90, 33, [70, 20]
