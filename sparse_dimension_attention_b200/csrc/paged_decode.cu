@@ -82,11 +82,11 @@ struct DecodeP {
   uint8_t* qpart;        // [n_units][N][D] e4m3 parts of the masked queries: row h * stride + part
   float* qfac;           // [n_units][kMaxG] factor of a head's scores (log2 domain, without the key scale)
   int32_t* prefix;       // [B + 1] tiles of one KV head before each sequence
-  int32_t* ctl;          // [0] pieces taken beyond the first ones, [1] pieces in all
+  int32_t* ctl;          // [0] pieces taken beyond the first ones, [1] units to merge
   float2* part_ml;       // [2 * pieces][G] (M, l) of a partial result
   float* part_o;         // [2 * pieces][G][D]
-  int4* split;           // [pieces] piece x starts inside unit .x, whose tiles lie in pieces .y ... .z; .w: slot of
-                         // piece .y's part; .x < 0: x starts with a unit
+  int4* split;           // [pieces] units to merge, in any order: unit .x has its tiles in pieces .y ... .z; .w: slot of
+                         // piece .y's part
 };
 
 __device__ __forceinline__ int n_tiles(int len) { return (len + TT - 1) / TT; }
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, 
   const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
   if (tid == 0) {
     if (bad) report_arg(c);
-    if (u == 0) p.ctl[0] = 0;
+    if (u == 0) p.ctl[0] = p.ctl[1] = 0;
     before = 0;
   }
   __syncthreads();
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     for (int y = 0; y < kThreads / 32; ++y) total += ms.scan[y];
   }
   const Pieces pieces(total * c.Hkv, gridDim.x);
-  if (blockIdx.x >= pieces.nb && blockIdx.x > 0) return;
-  if (pieces.nb > 0) {
+  if (blockIdx.x >= pieces.nb) return;
+  {
     const long long t0 = pieces.start(blockIdx.x);
     long long before = 0;
     for (int base = 0; base < c.B; base += kThreads) {
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     ms.abort = 0;
     for (int i = 0; i < kVStages; ++i) ms.info[i] = TileInfo{0, 0, 0, 0, 0, 0, 0, 0};
   }
-  if (w == kMmaWarp && pieces.nb > 0) {
+  if (w == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)),
                  "r"((uint32_t)CC::TMEM)
                  : "memory");
@@ -599,11 +599,6 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  if (pieces.nb == 0) {                       // no tokens at all (block 0)
-    pdl_wait();
-    if (tid == 0) p.ctl[1] = 0;
-    return;
-  }
 
   // page of 16 tokens of a tile, chunk `lane` (lanes 0..7 of a copying warp)
   auto page_of_chunk = [&](int b, int tile, int len) {
@@ -711,15 +706,14 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     int iu = -1, ord = -1;
     bool part_first = true, waited = false;    // the piece's first tile is next; the earlier kernels' results may be read
     int seg_first = 0;                         // first tile of the unit in this piece
-    // where a piece lies among the units it shares with others, for the merge
+    // A piece that is the second of a unit's pieces puts the unit on the list of the merge.
     auto note_split = [&]() {
-      int4 sp = make_int4(-1, 0, 0, 0);
-      if (cur.tile > 0) {
-        const long long f = begin - cur.tile;                 // the unit's tiles are [f, f + n)
-        const int first = pieces.of(f);
-        sp = make_int4(cur.u, first, pieces.of(f + n_tiles(cur.len) - 1), pieces.start(first) < f ? 1 : 0);
-      }
-      p.split[piece] = sp;
+      if (cur.tile == 0) return;
+      const long long f = begin - cur.tile;                   // the unit's tiles are [f, f + n)
+      const int first = pieces.of(f);
+      if (first != piece - 1) return;
+      p.split[atomicAdd(p.ctl + 1, 1)] =
+          make_int4(cur.u, first, pieces.of(f + n_tiles(cur.len) - 1), pieces.start(first) < f ? 1 : 0);
     };
     // The first value rows come while the selection runs; then its results, and the merge of an earlier call, which
     // has read its parts.
@@ -728,7 +722,6 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
       pdl_wait();
       pdl_launch_dependents();
       if (lane == 0) {
-        if (blockIdx.x == 0) p.ctl[1] = pieces.count();
         const Cursor now = cur;
         cur = ms.cur;                          // the first piece's start
         note_split();
@@ -1036,11 +1029,10 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 // merge of the parts of units that several blocks shared
 // ============================================================================
 
-// Blocks share the boundaries between pieces; the first boundary inside a unit
-// merges it, for one query head of the group.  Bound by the latency of two dependent
-// loads: which parts, and the parts (M, l and O together, eight at a time).  Each of eight warps
-// runs over every eighth part, a float4 of O per lane; then the eight results are
-// added in order.
+// Blocks share the (unit, query head) pairs of the list.  Bound by the latency of
+// two dependent loads: which parts, and the parts (M, l and O together, eight at a
+// time).  Each of eight warps runs over every eighth part, a float4 of O per lane;
+// then the eight results are added in order.
 constexpr int kMergeWarps = 8;
 constexpr int kMaxPieces = 2048;
 constexpr int kPiecesPerBlock = 4;         // one first piece and three later ones
@@ -1048,17 +1040,14 @@ constexpr int kPiecesPerBlock = 4;         // one first piece and three later on
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
   __shared__ __align__(16) float sum[kMergeWarps][D];
   __shared__ float2 ml[kMergeWarps];
-  const int hh = blockIdx.y, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int n_pieces = p.ctl[1];
-  int4 sps[kPiecesPerBlock];               // fetched along with their number: the array has room for every one asked for
-#pragma unroll
-  for (int y = 0; y < kPiecesPerBlock; ++y) sps[y] = p.split[min(1 + (int)(blockIdx.x + y * gridDim.x), kPiecesPerBlock * (int)gridDim.x - 1)];
-#pragma unroll
-  for (int y = 0; y < kPiecesPerBlock; ++y) {
-    const int x = 1 + blockIdx.x + y * gridDim.x;
-    const int4 sp = sps[y];
-    if (x >= n_pieces || sp.x < 0 || sp.y != x - 1) continue;
+  int4 sp = p.split[blockIdx.x / G];       // along with their number: the list has room for more than the blocks
+  const int n_jobs = p.ctl[1] * G;
+#pragma unroll 1
+  for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
+    const int hh = job % G;
+    if (job != (int)blockIdx.x) sp = p.split[job / G];
     const int n = sp.z - sp.y + 1;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1174,8 +1163,7 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
   if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK) return rc;
-  // 4 * blocks boundaries, which is as many as there are pieces
-  e = launch_pdl(paged_merge_kernel, dim3(blocks, G), dim3(kMergeWarps * 32), 0, st, c, p, G);
+  e = launch_pdl(paged_merge_kernel, dim3(blocks), dim3(kMergeWarps * 32), 0, st, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
   return check_launch("paged_merge_kernel");
 }
