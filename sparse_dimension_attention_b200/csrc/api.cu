@@ -64,6 +64,21 @@ int set_smem_limit(const void* kernel, int bytes, const char* name) {
   return AQUA_OK;
 }
 
+int set_largest_carveout(const void* kernel, const char* name) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "%s: cudaGetDevice: %s", name, cudaGetErrorString(e));
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, bool> done;       // (kernel, device)
+  std::lock_guard<std::mutex> lock(mu);
+  bool& d = done[std::make_pair(kernel, dev)];
+  if (d) return AQUA_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "cudaFuncSetAttribute(%s, carveout): %s", name, cudaGetErrorString(e));
+  d = true;
+  return AQUA_OK;
+}
+
 namespace {
 // cuTensorMapEncodeTiled from the driver, resolved once through the runtime
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {

@@ -31,6 +31,9 @@ int device_sm_count();
 // cudaFuncSetAttribute acts per device, so the library records, per (kernel,
 // device), the limit already set (thread-safe); later calls cost one lookup.
 int set_smem_limit(const void* kernel, int bytes, const char* name);
+// Have an SM that runs `kernel` split its memory as for the largest shared memory (per device, recorded likewise):
+// a kernel that needs much of it can start beside this one, where another split would have to be left first.
+int set_largest_carveout(const void* kernel, const char* name);
 template <typename... KArgs>
 int set_smem_limit(void (*kernel)(KArgs...), int bytes, const char* name) {
   return set_smem_limit(reinterpret_cast<const void*>(kernel), bytes, name);

@@ -1,6 +1,6 @@
 // One decode step of AQUA attention over the paged 8-bit cache.
 //
-// paged_select_kernel, one block per (sequence b, KV head g): for the group's
+// paged_select_kernel, a block per KV head g and a few sequences b: for the group's
 // query heads q~ = rope(q, len - 1) P (f64, rounded once), the k largest |q~_j|
 // (ties to the lower j), the union U of the kept dimensions as a bit mask, and the
 // masked queries in the layout the tensor cores take them.
@@ -111,188 +111,188 @@ __device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -I
 // rotation, projection, top-k
 // ============================================================================
 
-// A chain of latencies: everything that does not need the earlier kernels' results (P, in f64) is done before
-// the wait on them, and after the projection each head is one warp's business.
+// A chain of latencies: P is loaded before the wait on the earlier kernels, and after the projection each head is one
+// warp's business.  64 registers leave room for an attention block beside this one.
 // GP: the group size padded to 1, 2, 4 or 8 (rows G .. GP-1 are zeros and never stored).
 template <typename T, int GP>
-__global__ void __launch_bounds__(kSelThreads) paged_select_kernel(PagedView c, DecodeP p, int G, int NH, int stride, int parts) {
+__global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView c, DecodeP p, int G, int NH, int stride, int parts, int group) {
   constexpr int kSlices = kSelThreads / D, kRows = D / kSlices;      // P rows per thread
   __shared__ __align__(16) double qd[GP][D];       // rotated rows
   __shared__ double part[kSlices][GP][D];
   __shared__ float raw[GP][D];
   __shared__ uint32_t kept[GP][4];
   __shared__ int before;
-  const int u = blockIdx.x, b = u / c.Hkv, g = u % c.Hkv;
+  const int g = blockIdx.y;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int j = tid & 127, sl = tid >> 7;
   // P is read before the wait on the previous kernel: whatever may still run then does not write it
-  double pr[kRows];
+  float pr[kRows];
   {
     const float* Pg = p.P + (size_t)g * D * D + (size_t)sl * kRows * D + j;
-    float f[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) f[i] = __ldg(Pg + i * D);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      pr[i] = f[i];
-      asm volatile("" : "+d"(pr[i]));      // here, not behind the wait
-    }
+    for (int i = 0; i < kRows; ++i) pr[i] = __ldg(Pg + i * D);
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int len = __ldg(p.len + b);
-  const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
-  for (int i = tid; i < GP * D; i += kSelThreads)
-    raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
-  bool bad;
-  const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
-  if (tid == 0) {
-    if (bad) report_arg(c);
-    if (u == 0) p.ctl[0] = p.ctl[1] = 0;
-    before = 0;
-  }
-  __syncthreads();
-  for (int i = tid; i < GP * D; i += kSelThreads) {
-    const int hh = i >> 7;
-    const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
-    const double x = p.rope.cs != nullptr && n > 0 ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved)
-                                                   : (double)raw[hh][j];
-    qd[hh][j] = x;
-  }
-  __syncthreads();
-  {
-    // partial sums over kRows input dims of column j, all heads of the group
-    double acc[GP];
-#pragma unroll
-    for (int hh = 0; hh < GP; ++hh) acc[hh] = 0.0;
-#pragma unroll
-    for (int i = 0; i < kRows; i += 2) {
-#pragma unroll
-      for (int hh = 0; hh < GP; ++hh) {
-        const double2 qv = *reinterpret_cast<const double2*>(&qd[hh][sl * kRows + i]);
-        acc[hh] = fma(pr[i + 1], qv.y, fma(pr[i], qv.x, acc[hh]));
-      }
-    }
-#pragma unroll
-    for (int hh = 0; hh < GP; ++hh) part[sl][hh][j] = acc[hh];
-  }
-  __syncthreads();
-  if (w < G) {
-    // ---- head w: lane holds dims lane + 32 y
-    float qt[4];
-    uint32_t key[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int i = lane + 32 * y;
-      double sum = part[0][w][i];
-#pragma unroll
-      for (int x = 1; x < kSlices; ++x) sum += part[x][w][i];
-      qt[y] = (float)sum;
-      // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
-      key[y] = i < c.m ? min(__float_as_uint(fabsf(qt[y])), 0x7F800001u) + 1u : 0u;
-      if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G + w) * D + i] = qt[y];
-    }
-    // tau: the largest value with at least k keys >= tau, a bit a round from the top; the search ends when
-    // exactly k are
-    uint32_t tau = 0;
-    int cnt = D;
+  if (tid == 0 && blockIdx.x == 0 && g == 0) p.ctl[0] = p.ctl[1] = 0;
 #pragma unroll 1
-    for (int bit = 30; bit >= 0 && cnt != p.k; --bit) {
-      const uint32_t cand = tau | (1u << bit);
-      const int n_ge = __reduce_add_sync(0xffffffffu, (int)(key[0] >= cand) + (int)(key[1] >= cand) + (int)(key[2] >= cand) +
-                                                          (int)(key[3] >= cand));
-      if (n_ge >= p.k) {
-        tau = cand;
-        cnt = n_ge;
-      }
+  for (int b = blockIdx.x * group; b < min(c.B, ((int)blockIdx.x + 1) * group); ++b) {
+    const int u = b * c.Hkv + g;
+    const int len = __ldg(p.len + b);
+    const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
+    for (int i = tid; i < GP * D; i += kSelThreads)
+      raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
+    bool bad;
+    const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
+    if (tid == 0) {
+      if (bad) report_arg(c);
+      before = 0;
     }
-    uint32_t word[4];
+    __syncthreads();
+    for (int i = tid; i < GP * D; i += kSelThreads) {
+      const int hh = i >> 7;
+      const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
+      const double x = p.rope.cs != nullptr && n > 0 ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved)
+                                                     : (double)raw[hh][j];
+      qd[hh][j] = x;
+    }
+    __syncthreads();
+    {
+      // partial sums over kRows input dims of column j, all heads of the group
+      double acc[GP];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) word[y] = __ballot_sync(0xffffffffu, key[y] >= tau && key[y] > 0);
-    if (cnt != p.k) {
-      // equal keys straddle the cut: every key above tau, then keys equal to tau from the lowest dim up
-      int need = p.k;
+      for (int hh = 0; hh < GP; ++hh) acc[hh] = 0.0;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) need -= __popc(__ballot_sync(0xffffffffu, key[y] > tau));
+      for (int i = 0; i < kRows; i += 2) {
+        const double x0 = pr[i], x1 = pr[i + 1];
+#pragma unroll
+        for (int hh = 0; hh < GP; ++hh) {
+          const double2 qv = *reinterpret_cast<const double2*>(&qd[hh][sl * kRows + i]);
+          acc[hh] = fma(x1, qv.y, fma(x0, qv.x, acc[hh]));
+        }
+      }
+#pragma unroll
+      for (int hh = 0; hh < GP; ++hh) part[sl][hh][j] = acc[hh];
+    }
+    __syncthreads();
+    if (w < G) {
+      // ---- head w: lane holds dims lane + 32 y
+      float qt[4];
+      uint32_t key[4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const uint32_t eq = __ballot_sync(0xffffffffu, key[y] == tau && key[y] > 0);
-        const bool take = key[y] > tau || (key[y] == tau && key[y] > 0 && __popc(eq & ((1u << lane) - 1u)) < need);
-        need -= min(need, __popc(eq));
-        word[y] = __ballot_sync(0xffffffffu, take);
+        const int i = lane + 32 * y;
+        double sum = part[0][w][i];
+#pragma unroll
+        for (int x = 1; x < kSlices; ++x) sum += part[x][w][i];
+        qt[y] = (float)sum;
+        // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
+        key[y] = i < c.m ? min(__float_as_uint(fabsf(qt[y])), 0x7F800001u) + 1u : 0u;
+        if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G + w) * D + i] = qt[y];
+      }
+      // tau: the largest value with at least k keys >= tau, a bit a round from the top; the search ends when
+      // exactly k are
+      uint32_t tau = 0;
+      int cnt = D;
+#pragma unroll 1
+      for (int bit = 30; bit >= 0 && cnt != p.k; --bit) {
+        const uint32_t cand = tau | (1u << bit);
+        const int n_ge = __reduce_add_sync(0xffffffffu, (int)(key[0] >= cand) + (int)(key[1] >= cand) + (int)(key[2] >= cand) +
+                                                            (int)(key[3] >= cand));
+        if (n_ge >= p.k) {
+          tau = cand;
+          cnt = n_ge;
+        }
+      }
+      uint32_t word[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) word[y] = __ballot_sync(0xffffffffu, key[y] >= tau && key[y] > 0);
+      if (cnt != p.k) {
+        // equal keys straddle the cut: every key above tau, then keys equal to tau from the lowest dim up
+        int need = p.k;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) need -= __popc(__ballot_sync(0xffffffffu, key[y] > tau));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t eq = __ballot_sync(0xffffffffu, key[y] == tau && key[y] > 0);
+          const bool take = key[y] > tau || (key[y] == tau && key[y] > 0 && __popc(eq & ((1u << lane) - 1u)) < need);
+          need -= min(need, __popc(eq));
+          word[y] = __ballot_sync(0xffffffffu, take);
+        }
+      }
+      float mx = 0.f;
+      int pos = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const bool keep = (word[y] >> lane) & 1u;
+        if (keep) {
+          if (p.sel_out)
+            p.sel_out[((size_t)b * p.Hq + (size_t)g * G + w) * p.k + pos + __popc(word[y] & ((1u << lane) - 1u))] = lane + 32 * y;
+          mx = fmaxf(mx, finite_abs(qt[y]));
+        } else {
+          qt[y] = 0.f;
+        }
+        pos += __popc(word[y]);
+        if (lane == 0) kept[w][y] = word[y];
+      }
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      if (lane == 0) p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
+      // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
+      // most half a step, so 16 times it stays in range)
+      uint8_t* dst = p.qpart + ((size_t)u * NH + w) * stride * D + lane;
+#pragma unroll
+      for (int y = 0; y < 4; y += 2) {
+        float x0 = qt[y] * mul, x1 = qt[y + 1] * mul;
+        if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // an infinite query makes its scores NaN, not the largest code
+        if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+        for (int i = 0; i < stride; ++i) {
+          const uint16_t code = i < parts ? f32x2_to_e4m3x2(x0, x1) : (uint16_t)0;
+          dst[i * D + 32 * y] = (uint8_t)code;
+          dst[i * D + 32 * y + 32] = (uint8_t)(code >> 8);
+          const float2 back = e4m3x2_to_f32x2(code);
+          x0 = (x0 - back.x) * 16.f;
+          x1 = (x1 - back.y) * 16.f;
+        }
+      }
+    } else if (w >= 8) {
+      // zeros for the heads the operand has room for but the group lacks
+      for (int i = tid - 256; i < (NH - G) * stride * (D / 16); i += kSelThreads - 256)
+        reinterpret_cast<uint4*>(p.qpart + ((size_t)u * NH + G) * stride * D)[i] = make_uint4(0, 0, 0, 0);
+      // tiles of the sequences before this one (one block of each sequence)
+      if (g == 0) {
+        int sum = 0;
+        for (int x = tid - 256; x < b; x += kSelThreads - 256) sum += n_tiles(seq_tokens(c, p, x));
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0 && sum != 0) atomicAdd(&before, sum);
       }
     }
-    float mx = 0.f;
-    int pos = 0;
+    __syncthreads();
+    if (tid == 0) {
+      uint4 um = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const bool keep = (word[y] >> lane) & 1u;
-      if (keep) {
-        if (p.sel_out)
-          p.sel_out[((size_t)b * p.Hq + (size_t)g * G + w) * p.k + pos + __popc(word[y] & ((1u << lane) - 1u))] = lane + 32 * y;
-        mx = fmaxf(mx, finite_abs(qt[y]));
-      } else {
-        qt[y] = 0.f;
+      for (int hh = 0; hh < GP; ++hh) {
+        if (hh >= G) break;
+        um.x |= kept[hh][0];
+        um.y |= kept[hh][1];
+        um.z |= kept[hh][2];
+        um.w |= kept[hh][3];
       }
-      pos += __popc(word[y]);
-      if (lane == 0) kept[w][y] = word[y];
-    }
-    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-    // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
-    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
-    const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-    if (lane == 0) p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
-    // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
-    // most half a step, so 16 times it stays in range)
-    uint8_t* dst = p.qpart + ((size_t)u * NH + w) * stride * D + lane;
-#pragma unroll
-    for (int y = 0; y < 4; y += 2) {
-      float x0 = qt[y] * mul, x1 = qt[y + 1] * mul;
-      if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // an infinite query makes its scores NaN, not the largest code
-      if (!(fabsf(x1) < INFINITY)) x1 = NAN;
-      for (int i = 0; i < stride; ++i) {
-        const uint16_t code = i < parts ? f32x2_to_e4m3x2(x0, x1) : (uint16_t)0;
-        dst[i * D + 32 * y] = (uint8_t)code;
-        dst[i * D + 32 * y + 32] = (uint8_t)(code >> 8);
-        const float2 back = e4m3x2_to_f32x2(code);
-        x0 = (x0 - back.x) * 16.f;
-        x1 = (x1 - back.y) * 16.f;
+      p.umask[u] = um;
+      if (g == 0) {
+        p.prefix[b] = before;
+        if (b == c.B - 1) p.prefix[c.B] = before + n_tiles(n);
       }
     }
-  } else if (w >= 8) {
-    // zeros for the heads the operand has room for but the group lacks
-    for (int i = tid - 256; i < (NH - G) * stride * (D / 16); i += kSelThreads - 256)
-      reinterpret_cast<uint4*>(p.qpart + ((size_t)u * NH + G) * stride * D)[i] = make_uint4(0, 0, 0, 0);
-    // tiles of the sequences before this one (one block of each sequence)
-    if (g == 0) {
-      int sum = 0;
-      for (int x = tid - 256; x < b; x += kSelThreads - 256) sum += n_tiles(seq_tokens(c, p, x));
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      if (lane == 0 && sum != 0) atomicAdd(&before, sum);
+    // an empty sequence has no tiles: attention over no token is 0 with lse -inf
+    if (n == 0) {
+      const size_t r0 = (size_t)b * p.Hq + (size_t)g * G;
+      for (int i = tid; i < G * D; i += kSelThreads) store_out_elem(p, r0 * D + i, 0.f);
+      if (p.lse_out && tid < G) p.lse_out[r0 + tid] = -INFINITY;
     }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    uint4 um = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int hh = 0; hh < GP; ++hh) {
-      if (hh >= G) break;
-      um.x |= kept[hh][0];
-      um.y |= kept[hh][1];
-      um.z |= kept[hh][2];
-      um.w |= kept[hh][3];
-    }
-    p.umask[u] = um;
-    if (g == 0) {
-      p.prefix[b] = before;
-      if (b == c.B - 1) p.prefix[c.B] = before + n_tiles(n);
-    }
-  }
-  // an empty sequence has no tiles: attention over no token is 0 with lse -inf
-  if (n == 0) {
-    const size_t r0 = (size_t)b * p.Hq + (size_t)g * G;
-    for (int i = tid; i < G * D; i += kSelThreads) store_out_elem(p, r0 * D + i, 0.f);
-    if (p.lse_out && tid < G) p.lse_out[r0 + tid] = -INFINITY;
+    __syncthreads();
   }
 }
 
@@ -1137,13 +1137,24 @@ int attend_blocks(int per_sm) {
   return n < kMaxPieces / kPiecesPerBlock ? n : kMaxPieces / kPiecesPerBlock;
 }
 
+template <typename T, int GP>
+cudaError_t launch_select_as(dim3 grid, const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, int group,
+                             cudaStream_t st) {
+  const auto kernel = paged_select_kernel<T, GP>;
+  if (set_largest_carveout(reinterpret_cast<const void*>(kernel), "paged_select_kernel") != AQUA_OK) return cudaErrorUnknown;
+  return launch_pdl(kernel, grid, dim3(kSelThreads), 0, st, c, p, G, NH, stride, parts, group);
+}
+
 template <typename T>
 cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
-  const dim3 grid(c.B * c.Hkv), block(kSelThreads);
-  if (G == 1) return launch_pdl(paged_select_kernel<T, 1>, grid, block, 0, st, c, p, G, NH, stride, parts);
-  if (G == 2) return launch_pdl(paged_select_kernel<T, 2>, grid, block, 0, st, c, p, G, NH, stride, parts);
-  if (G <= 4) return launch_pdl(paged_select_kernel<T, 4>, grid, block, 0, st, c, p, G, NH, stride, parts);
-  return launch_pdl(paged_select_kernel<T, 8>, grid, block, 0, st, c, p, G, NH, stride, parts);
+  // As many sequences a block as leave one block an SM: P is read once for all of them, and an attention block
+  // fits beside it and fetches its first tiles.  (256 units, two blocks an SM: selection 10 us, attention from 11 us.)
+  const int sms = device_sm_count(), group = (c.B * c.Hkv + sms - 1) / sms;
+  const dim3 grid((c.B + group - 1) / group, c.Hkv);
+  if (G == 1) return launch_select_as<T, 1>(grid, c, p, G, NH, stride, parts, group, st);
+  if (G == 2) return launch_select_as<T, 2>(grid, c, p, G, NH, stride, parts, group, st);
+  if (G <= 4) return launch_select_as<T, 4>(grid, c, p, G, NH, stride, parts, group, st);
+  return launch_select_as<T, 8>(grid, c, p, G, NH, stride, parts, group, st);
 }
 
 template <int STR, int NH>
@@ -1163,6 +1174,8 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
   if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK) return rc;
+  rc = set_largest_carveout(reinterpret_cast<const void*>(paged_merge_kernel), "paged_merge_kernel");
+  if (rc != AQUA_OK) return rc;
   e = launch_pdl(paged_merge_kernel, dim3(blocks), dim3(kMergeWarps * 32), 0, st, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
   return check_launch("paged_merge_kernel");
