@@ -23,7 +23,8 @@ struct GatherParams {
   int Tcap, max_len;
 };
 
-// sixteen codes times s, stored as sixteen consecutive elements (the first n of them)
+// Sixteen codes times s, stored as sixteen consecutive elements (the first n of them).  All lanes of a warp call it,
+// neighbours with neighbouring destinations.
 __device__ __forceinline__ void store16(float* p, const uint4& w, float s, int n) {
   const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
@@ -49,7 +50,19 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& w, float 
     y[2 * i] = pack_bf16(a.x * s, a.y * s);
     y[2 * i + 1] = pack_bf16(b.x * s, b.y * s);
   }
-  if (n >= 16) {
+  // A lane has two 16-byte pieces.  Even and odd lanes trade one each, so that a store of the warp covers
+  // pieces that lie side by side: first the even lanes' 32 bytes, then the odd lanes'.
+  const bool odd = threadIdx.x & 1, pair = __all_sync(0xffffffffu, n >= 16);
+  if (pair) {
+    const uint64_t mine = reinterpret_cast<uint64_t>(p), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    uint32_t got[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) got[i] = __shfl_xor_sync(0xffffffffu, odd ? y[i] : y[4 + i], 1);
+    uint4* const e = reinterpret_cast<uint4*>(odd ? other : mine);           // the even lane's place
+    uint4* const o = reinterpret_cast<uint4*>(odd ? mine : other);
+    e[odd] = odd ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(y[0], y[1], y[2], y[3]);
+    o[odd] = odd ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(got[0], got[1], got[2], got[3]);
+  } else if (n >= 16) {
     reinterpret_cast<uint4*>(p)[0] = make_uint4(y[0], y[1], y[2], y[3]);
     reinterpret_cast<uint4*>(p)[1] = make_uint4(y[4], y[5], y[6], y[7]);
   } else {
@@ -73,45 +86,54 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedView c, Gat
   }
   if (t0 >= n) return;
   __shared__ int pids[kTok / 16];
+  __shared__ float scales[2][kTok / 16];
   if (threadIdx.x < kTok / 16) {
     const int t = t0 + 16 * threadIdx.x;
     int pid = -1;
+    float ks = 0.f, vs = 0.f;
     if (t < n) {
       pid = __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2));
-      if (pid < 0 || pid >= c.n_pages) {
+      if (pid >= 0 && pid < c.n_pages) {
+        ks = __ldg(c.ks + (size_t)pid * c.Hkv + h);
+        vs = __ldg(c.vs + (size_t)pid * c.Hkv + h);
+      } else {
         pid = -1;
         report_arg(c);
       }
     }
     pids[threadIdx.x] = pid;
+    scales[0][threadIdx.x] = ks;
+    scales[1][threadIdx.x] = vs;
   }
   __syncthreads();
   const int nt = min(kTok, n - t0), mask = (1 << c.page_log2) - 1;
   const size_t unit = (size_t)i * c.Hkv + h;
-  T* kd = static_cast<T*>(g.k) + unit * c.m * (size_t)g.Tcap;
-  T* vd = static_cast<T*>(g.v) + unit * (size_t)g.Tcap * D;
-  for (int x = threadIdx.x; x < c.m * (kTok / 16); x += kThreads) {        // (dimension, 16 tokens)
-    const int j = x >> 3, cc = x & 7, t = 16 * cc;
-    if (t >= nt) continue;
-    const int pid = pids[cc];
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
-    if (pid >= 0) {
-      w = __ldg(reinterpret_cast<const uint4*>(c.k + c.kblock(pid, h) + ((size_t)j << c.page_log2) + ((t0 + t) & mask)));
-      s = __ldg(c.ks + (size_t)pid * c.Hkv + h);
-    }
-    store16(kd + (size_t)j * g.Tcap + t0 + t, w, s, nt - t);
+  T* kd = static_cast<T*>(g.k) + unit * c.m * (size_t)g.Tcap + t0;
+  T* vd = static_cast<T*>(g.v) + (unit * (size_t)g.Tcap + t0) * D;
+  // A thread has piece cc of up to four dims (16 tokens each) and of up to four tokens (16 dims each): all eight
+  // loads are in flight before the first store.
+  constexpr int kEach = D * (kTok / 16) / kThreads;
+  const int cc = threadIdx.x & 7, r0 = threadIdx.x >> 3, kpid = pids[cc];
+  uint4 kw[kEach], vw[kEach];
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) {
+    const int j = r0 + y * (kThreads / 8);                     // dim, token
+    kw[y] = vw[y] = make_uint4(0, 0, 0, 0);
+    if (j < c.m && kpid >= 0)
+      kw[y] = __ldg(reinterpret_cast<const uint4*>(c.k + c.kblock(kpid, h) + ((size_t)j << c.page_log2) + ((t0 + 16 * cc) & mask)));
+    const int vpid = pids[j >> 4];
+    if (j < nt && vpid >= 0)
+      vw[y] = __ldg(reinterpret_cast<const uint4*>(c.v + c.vblock(vpid, h) + (size_t)((t0 + j) & mask) * D) + cc);
   }
-  for (int x = threadIdx.x; x < nt * (D / 16); x += kThreads) {            // (token, 16 dimensions)
-    const int t = x >> 3, cc = x & 7;
-    const int pid = pids[t >> 4];
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
-    if (pid >= 0) {
-      w = __ldg(reinterpret_cast<const uint4*>(c.v + c.vblock(pid, h) + (size_t)((t0 + t) & mask) * D) + cc);
-      s = __ldg(c.vs + (size_t)pid * c.Hkv + h);
-    }
-    store16(vd + (size_t)(t0 + t) * D + 16 * cc, w, s, 16);
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) {
+    const int j = r0 + y * (kThreads / 8);
+    store16(kd + (size_t)j * g.Tcap + 16 * cc, kw[y], scales[0][cc], j < c.m ? nt - 16 * cc : 0);
+  }
+#pragma unroll
+  for (int y = 0; y < kEach; ++y) {
+    const int j = r0 + y * (kThreads / 8);
+    store16(vd + (size_t)j * D + 16 * cc, vw[y], scales[1][j >> 4], j < nt ? 16 : 0);
   }
 }
 
