@@ -1149,7 +1149,8 @@ template <typename T>
 cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
   // As many sequences a block as leave one block an SM: P is read once for all of them, and an attention block
   // fits beside it and fetches its first tiles.  (256 units, two blocks an SM: selection 10 us, attention from 11 us.)
-  const int sms = device_sm_count(), group = (c.B * c.Hkv + sms - 1) / sms;
+  const int each = device_sm_count() / c.Hkv > 0 ? device_sm_count() / c.Hkv : 1;     // blocks a head
+  const int group = (c.B + each - 1) / each;
   const dim3 grid((c.B + group - 1) / group, c.Hkv);
   if (G == 1) return launch_select_as<T, 1>(grid, c, p, G, NH, stride, parts, group, st);
   if (G == 2) return launch_select_as<T, 2>(grid, c, p, G, NH, stride, parts, group, st);
