@@ -286,9 +286,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
 // both factors split into two f16 parts (x_l P_h + x_h P_l + x_h P_h, f32
 // accumulation): rows and P are first brought to [2^10, 2^11) by powers of two,
 // so the parts hold 22 bits and the dropped product is below 2^-22 of a term.
-// The tensor cores cut every sum they extend off to 24 bits, which makes a chain
-// of 24 products, the small ones first, 2.3e-7 off (2-norm): as an f32 sum of
-// 128 terms (2.0e-7; exact sums of the same parts: 0.7e-7).
+// The tensor cores cut every sum they extend off to 24 bits, which makes one chain
+// of 24 products 2.3e-7 off (2-norm; an f32 sum of 128 terms 2.0e-7, exact sums of
+// the same parts 0.7e-7).  So two accumulators of 64 input dims each, the small
+// products first, added in f32: 1.5e-7.
 //
 // What bounds it is the arithmetic around the products (some 20 instructions an
 // element), so the roles overlap: warps 0-7 rotate, normalise and split the rows
@@ -397,11 +398,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]));                  // not before the wait
-}
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[32], uint32_t (&b)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
@@ -507,8 +503,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
     ms.pmax = 0;
   }
   if (w == kProdWarp) {
-    // 128 columns for each of two tiles
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)), "r"(256u)
+    // two accumulators of 128 columns for each of two tiles
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms.tmem)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -733,8 +729,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
           const uint64_t bd = desc_sw128(pa + (pr == 1 ? kPart : 0), kTile * 128);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_f16(tmem + buf * D, ad + (uint64_t)(((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
-                    bd + (uint64_t)((ks * 16 * 128) >> 4), idesc, pr > 0 || ks > 0);
+            mma_f16(tmem + buf * 2 * D + (ks >> 2) * D, ad + (uint64_t)(((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),
+                    bd + (uint64_t)((ks * 16 * 128) >> 4), idesc, pr > 0 || (ks & 3));
         }
         commit_to(&ms.x_free[buf]);
         commit_to(&ms.d_full[buf]);
@@ -756,26 +752,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
       tile_wait(&ms.d_full[buf], (t >> 1) & 1, ms, c.ctrl);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // tensor memory is read twice, for the maxima and for the codes: 128 numbers do not fit the registers
-      const uint32_t col = tmem + ((uint32_t)(32 * (w & 3)) << 16) + buf * D;
+      const uint32_t col = tmem + ((uint32_t)(32 * (w & 3)) << 16) + buf * 2 * D;
       const float unit = ms.unit[t & 3][kr];
       float km = 0.f;
 #pragma unroll 1
-      for (int q = 0; q < D; q += 64) {
+      for (int q = 0; q < D; q += 32) {
         uint32_t x[32], y[32];
         tmem_ld32(col + q, x);
-        tmem_ld32(col + q + 32, y);
+        tmem_ld32(col + D + q, y);
         tmem_wait_ld(x, y);
         float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e])), fabsf(__uint_as_float(y[e]))));
+        for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(__uint_as_float(x[e]) + __uint_as_float(y[e])));
         if (!(m * unit < INFINITY)) {        // an infinity among them: the largest finite one
           m = 0.f;
 #pragma unroll 1
-          for (int e = 0; e < 64; ++e) {
-            uint32_t z;
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
-                         : "=r"(z) : "r"(col + q + e) : "memory");
-            if (fabsf(__uint_as_float(z)) * unit < INFINITY) m = fmaxf(m, fabsf(__uint_as_float(z)));
+          for (int e = 0; e < 32; ++e) {
+            uint32_t z0, z1;
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(z0) : "r"(col + q + e) : "memory");
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(z1) : "r"(col + D + q + e) : "memory");
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            asm volatile("" : "+r"(z0), "+r"(z1));
+            const float k = fabsf(__uint_as_float(z0) + __uint_as_float(z1));
+            if (k * unit < INFINITY) m = fmaxf(m, k);
           }
         }
         km = fmaxf(km, m);
@@ -794,13 +793,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
         const int row = 1 << c.page_log2;    // bytes from a dimension to the next
 #pragma unroll 1
         for (int q = 0; q < c.m; q += 32) {
-          uint32_t x[32];
+          uint32_t x[32], y[32];
           tmem_ld32(col + q, x);
-          tmem_wait_ld(x);
+          tmem_ld32(col + D + q, y);
+          tmem_wait_ld(x, y);
           uint8_t* d = dst + q * row;
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {  // dims past d_store fall into the buffer's padding
-            const uint16_t code = f32x2_to_e4m3x2(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f);
+            const uint16_t code = f32x2_to_e4m3x2((__uint_as_float(x[e]) + __uint_as_float(y[e])) * f,
+                                                  (__uint_as_float(x[e + 1]) + __uint_as_float(y[e + 1])) * f);
             d[e * row] = (uint8_t)code;
             d[(e + 1) * row] = (uint8_t)(code >> 8);
           }
@@ -943,7 +944,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (w == kProdWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 template <typename T, int MODE>
