@@ -111,68 +111,89 @@ __device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -I
 // rotation, projection, top-k
 // ============================================================================
 
-// A chain of latencies: P is loaded before the wait on the earlier kernels, and after the projection each head is one
-// warp's business.  64 registers leave room for an attention block beside this one.
-// GP: the group size padded to 1, 2, 4 or 8 (rows G .. GP-1 are zeros and never stored).
-template <typename T, int GP>
+// The projection runs on the f64 matrix instruction, heads as rows (those past G are zeros), eight columns of P a
+// warp: on f64 FMAs, every thread a column and all heads, the reads of q~ from shared memory took 5 of 7 us a
+// sequence.  What is left is a chain of latencies: P is loaded before the wait on the earlier kernels, the next
+// sequence's queries during this one's projection, and after it each head is one warp's business.  64 registers
+// leave room for an attention block, or a second block of this kernel, beside this one.
+__device__ __forceinline__ void mma_f64(double2& d, double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+               : "+d"(d.x), "+d"(d.y)
+               : "d"(a), "d"(b));
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView c, DecodeP p, int G, int NH, int stride, int parts, int group) {
-  constexpr int kSlices = kSelThreads / D, kRows = D / kSlices;      // P rows per thread
-  __shared__ __align__(16) double qd[GP][D];       // rotated rows
-  __shared__ double part[kSlices][GP][D];
-  __shared__ float raw[GP][D];
-  __shared__ uint32_t kept[GP][4];
+  static_assert(kSelThreads == 4 * D && kMaxG == 8, "eight columns a warp, eight rows an instruction");
+  constexpr int kEach = kMaxG * D / kSelThreads;      // elements of the group's queries a thread
+  __shared__ __align__(16) double qd[kMaxG][D + 8];   // rotated rows; the pad keeps the fragments' reads apart
+  __shared__ float raw[kMaxG][D], qs[kMaxG][D];
+  __shared__ uint32_t kept[kMaxG][4];
   __shared__ int before;
   const int g = blockIdx.y;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  const int j = tid & 127, sl = tid >> 7;
+  // fragment of the instruction: row (head) or column lane / 4; input dims 8 s + 2 (lane % 4), + 1 for step 2 s, 2 s + 1
+  const int fr = lane >> 2, fk = 2 * (lane & 3);
   // P is read before the wait on the previous kernel: whatever may still run then does not write it
-  float pr[kRows];
+  float pr[D / 4];
   {
-    const float* Pg = p.P + (size_t)g * D * D + (size_t)sl * kRows * D + j;
+    const float* Pg = p.P + (size_t)g * D * D + (size_t)fk * D + 8 * w + fr;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) pr[i] = __ldg(Pg + i * D);
+    for (int i = 0; i < D / 4; i += 2) {
+      pr[i] = __ldg(Pg + 4 * i * D);
+      pr[i + 1] = __ldg(Pg + 4 * i * D + D);
+    }
   }
+  for (int i = tid; i < kMaxG * (D + 8); i += kSelThreads) qd[0][i] = 0.0;
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x == 0 && g == 0) p.ctl[0] = p.ctl[1] = 0;
-#pragma unroll 1
-  for (int b = blockIdx.x * group; b < min(c.B, ((int)blockIdx.x + 1) * group); ++b) {
-    const int u = b * c.Hkv + g;
-    const int len = __ldg(p.len + b);
+  const int b_end = min(c.B, ((int)blockIdx.x + 1) * group);
+  int len = 0;
+  float x[kEach];
+  auto fetch = [&](int b) {
+    len = __ldg(p.len + b);
     const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
-    for (int i = tid; i < GP * D; i += kSelThreads)
-      raw[i >> 7][i & 127] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
+#pragma unroll
+    for (int y = 0; y < kEach; ++y) {
+      const int i = tid + y * kSelThreads;
+      x[y] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
+    }
+  };
+  fetch(blockIdx.x * group);
+#pragma unroll 1
+  for (int b = blockIdx.x * group; b < b_end; ++b) {
+    const int u = b * c.Hkv + g;
     bool bad;
     const int n = checked_len(len, c, p.rope.cs ? p.rope.n_pos : 0x7fffffff, bad);
+    const bool turn = p.rope.cs != nullptr && n > 0;
+    if (turn) {
+#pragma unroll
+      for (int y = 0; y < kEach; ++y) raw[(tid + y * kSelThreads) >> 7][tid & 127] = x[y];
+    }
     if (tid == 0) {
       if (bad) report_arg(c);
       before = 0;
     }
     __syncthreads();
-    for (int i = tid; i < GP * D; i += kSelThreads) {
-      const int hh = i >> 7;
-      const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
-      const double x = p.rope.cs != nullptr && n > 0 ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved)
-                                                     : (double)raw[hh][j];
-      qd[hh][j] = x;
+    const float* cs = p.rope.cs + (size_t)(n - 1) * p.rope.rot;
+#pragma unroll
+    for (int y = 0; y < kEach; ++y) {
+      const int hh = (tid + y * kSelThreads) >> 7, j = tid & 127;
+      if (hh < G) qd[hh][j] = turn ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved) : (double)x[y];
     }
     __syncthreads();
+    if (b + 1 < b_end) fetch(b + 1);
     {
-      // partial sums over kRows input dims of column j, all heads of the group
-      double acc[GP];
+      double2 even = make_double2(0.0, 0.0), odd = make_double2(0.0, 0.0);
 #pragma unroll
-      for (int hh = 0; hh < GP; ++hh) acc[hh] = 0.0;
-#pragma unroll
-      for (int i = 0; i < kRows; i += 2) {
-        const double x0 = pr[i], x1 = pr[i + 1];
-#pragma unroll
-        for (int hh = 0; hh < GP; ++hh) {
-          const double2 qv = *reinterpret_cast<const double2*>(&qd[hh][sl * kRows + i]);
-          acc[hh] = fma(x1, qv.y, fma(x0, qv.x, acc[hh]));
-        }
+      for (int i = 0; i < D / 4; i += 2) {
+        const double2 a = *reinterpret_cast<const double2*>(&qd[fr][4 * i + fk]);
+        mma_f64(even, a.x, (double)pr[i]);
+        mma_f64(odd, a.y, (double)pr[i + 1]);
       }
-#pragma unroll
-      for (int hh = 0; hh < GP; ++hh) part[sl][hh][j] = acc[hh];
+      // row fr, columns 8 w + fk, + 1
+      *reinterpret_cast<float2*>(&qs[fr][8 * w + fk]) = make_float2((float)(even.x + odd.x), (float)(even.y + odd.y));
     }
     __syncthreads();
     if (w < G) {
@@ -182,10 +203,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int i = lane + 32 * y;
-        double sum = part[0][w][i];
-#pragma unroll
-        for (int x = 1; x < kSlices; ++x) sum += part[x][w][i];
-        qt[y] = (float)sum;
+        qt[y] = qs[w][i];
         // magnitude order as unsigned order; dims past d_store below every candidate, NaN payloads one key
         key[y] = i < c.m ? min(__float_as_uint(fabsf(qt[y])), 0x7F800001u) + 1u : 0u;
         if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G + w) * D + i] = qt[y];
@@ -273,7 +291,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
     if (tid == 0) {
       uint4 um = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int hh = 0; hh < GP; ++hh) {
+      for (int hh = 0; hh < kMaxG; ++hh) {
         if (hh >= G) break;
         um.x |= kept[hh][0];
         um.y |= kept[hh][1];
@@ -1035,6 +1053,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 // then the eight results are added in order.
 constexpr int kMergeWarps = 8;
 constexpr int kMaxPieces = 2048;
+constexpr int kMergeFew = 8;
 constexpr int kPiecesPerBlock = 4;         // one first piece and three later ones
 
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
@@ -1044,11 +1063,53 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView
   pdl_wait();
   int4 sp = p.split[blockIdx.x / G];       // along with their number: the list has room for more than the blocks
   const int n_jobs = p.ctl[1] * G;
+  // units cut in eight parts or fewer: a warp each
+#pragma unroll 1
+  for (int job = blockIdx.x * kMergeWarps + w; job < n_jobs; job += gridDim.x * kMergeWarps) {
+    const int hh = job % G;
+    const int4 s1 = p.split[job / G];
+    const int n = s1.z - s1.y + 1;
+    if (n > kMergeFew) continue;
+    float2 m[kMergeFew];
+    float4 v[kMergeFew];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMergeFew; ++i) {
+      m[i] = make_float2(-INFINITY, 0.f);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const size_t slot = (size_t)(2 * (s1.y + i) + (i == 0 ? s1.w : 0)) * G + hh;
+        m[i] = p.part_ml[slot];
+        v[i] = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeFew; ++i) top = fmaxf(top, m[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kMergeFew; ++i) {
+      const float f = fast_exp2(m[i].x - ref);
+      L = fmaf(m[i].y, f, L);
+      acc.x = fmaf(v[i].x, f, acc.x); acc.y = fmaf(v[i].y, f, acc.y);
+      acc.z = fmaf(v[i].z, f, acc.z); acc.w = fmaf(v[i].w, f, acc.w);
+    }
+    const size_t row = (size_t)(s1.x / c.Hkv) * p.Hq + (size_t)(s1.x % c.Hkv) * G + hh;
+    const size_t at = row * D + 4 * lane;
+    store_out_elem(p, at, normalised(acc.x, L));
+    store_out_elem(p, at + 1, normalised(acc.y, L));
+    store_out_elem(p, at + 2, normalised(acc.z, L));
+    store_out_elem(p, at + 3, normalised(acc.w, L));
+    if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(top, L);
+  }
+  // the others: a block each
 #pragma unroll 1
   for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
     const int hh = job % G;
     if (job != (int)blockIdx.x) sp = p.split[job / G];
     const int n = sp.z - sp.y + 1;
+    if (n <= kMergeFew) continue;
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -1137,25 +1198,22 @@ int attend_blocks(int per_sm) {
   return n < kMaxPieces / kPiecesPerBlock ? n : kMaxPieces / kPiecesPerBlock;
 }
 
-template <typename T, int GP>
-cudaError_t launch_select_as(dim3 grid, const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, int group,
-                             cudaStream_t st) {
-  const auto kernel = paged_select_kernel<T, GP>;
-  if (set_largest_carveout(reinterpret_cast<const void*>(kernel), "paged_select_kernel") != AQUA_OK) return cudaErrorUnknown;
-  return launch_pdl(kernel, grid, dim3(kSelThreads), 0, st, c, p, G, NH, stride, parts, group);
-}
-
 template <typename T>
-cudaError_t launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
+int launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
   // As many sequences a block as leave one block an SM: P is read once for all of them, and an attention block
   // fits beside it and fetches its first tiles.  (256 units, two blocks an SM: selection 10 us, attention from 11 us.)
-  const int each = device_sm_count() / c.Hkv > 0 ? device_sm_count() / c.Hkv : 1;     // blocks a head
+  // With three sequences a block or more the selection itself is what takes long, and two blocks an SM overlap.
+  const int sms = device_sm_count();
+  const int waves = (long long)c.B * c.Hkv > 2 * sms ? 2 : 1;
+  const int each = waves * sms / c.Hkv > 0 ? waves * sms / c.Hkv : 1;                 // blocks a head
   const int group = (c.B + each - 1) / each;
   const dim3 grid((c.B + group - 1) / group, c.Hkv);
-  if (G == 1) return launch_select_as<T, 1>(grid, c, p, G, NH, stride, parts, group, st);
-  if (G == 2) return launch_select_as<T, 2>(grid, c, p, G, NH, stride, parts, group, st);
-  if (G <= 4) return launch_select_as<T, 4>(grid, c, p, G, NH, stride, parts, group, st);
-  return launch_select_as<T, 8>(grid, c, p, G, NH, stride, parts, group, st);
+  const auto kernel = paged_select_kernel<T>;
+  const int rc = set_largest_carveout(reinterpret_cast<const void*>(kernel), "paged_select_kernel");
+  if (rc != AQUA_OK) return rc;
+  const cudaError_t e = launch_pdl(kernel, grid, dim3(kSelThreads), 0, st, c, p, G, NH, stride, parts, group);
+  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
+  return check_launch("paged_select_kernel");
 }
 
 template <int STR, int NH>
@@ -1168,11 +1226,9 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   CUtensorMap vmap;
   rc = encode_tmap_bf16_2d(&vmap, c.v, D / 2, (uint64_t)c.n_pages * c.Hkv << c.page_log2, D, D / 2, c.page, true);
   if (rc != AQUA_OK) return rc;
-  cudaError_t e = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NH, STR, CC::QPARTS, st)
-                       : launch_select<float>(c, p, G, NH, STR, CC::QPARTS, st);
-  if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_select_kernel: %s", cudaGetErrorString(e));
-  if ((rc = check_launch("paged_select_kernel")) != AQUA_OK) return rc;
-  e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
+  rc = bf16 ? launch_select<__nv_bfloat16>(c, p, G, NH, STR, CC::QPARTS, st) : launch_select<float>(c, p, G, NH, STR, CC::QPARTS, st);
+  if (rc != AQUA_OK) return rc;
+  cudaError_t e = launch_pdl(paged_attend_kernel<STR, NH>, dim3(blocks), dim3(kThreads), smem, st, vmap, c, p, G);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_attend_kernel: %s", cudaGetErrorString(e));
   if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK) return rc;
   rc = set_largest_carveout(reinterpret_cast<const void*>(paged_merge_kernel), "paged_merge_kernel");
