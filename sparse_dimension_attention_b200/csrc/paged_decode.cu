@@ -150,14 +150,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
   if (tid == 0 && blockIdx.x == 0 && g == 0) p.ctl[0] = p.ctl[1] = 0;
   const int b_end = min(c.B, ((int)blockIdx.x + 1) * group);
   int len = 0;
-  float x[kEach];
+  T x[kEach];                               // as it lies in memory: a conversion here would wait for the load
   auto fetch = [&](int b) {
     len = __ldg(p.len + b);
     const T* q = static_cast<const T*>(p.q) + (size_t)b * p.qs.row + (size_t)g * G * p.qs.head;
 #pragma unroll
     for (int y = 0; y < kEach; ++y) {
       const int i = tid + y * kSelThreads;
-      x[y] = (i >> 7) < G ? Elem<T>::load(q + (size_t)(i >> 7) * p.qs.head + (i & 127)) : 0.f;
+      if ((i >> 7) < G) x[y] = q[(size_t)(i >> 7) * p.qs.head + (i & 127)];
     }
   };
   fetch(blockIdx.x * group);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
     const bool turn = p.rope.cs != nullptr && n > 0;
     if (turn) {
 #pragma unroll
-      for (int y = 0; y < kEach; ++y) raw[(tid + y * kSelThreads) >> 7][tid & 127] = x[y];
+      for (int y = 0; y < kEach; ++y) raw[(tid + y * kSelThreads) >> 7][tid & 127] = (float)x[y];
     }
     if (tid == 0) {
       if (bad) report_arg(c);
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
 #pragma unroll
     for (int y = 0; y < kEach; ++y) {
       const int hh = (tid + y * kSelThreads) >> 7, j = tid & 127;
-      if (hh < G) qd[hh][j] = turn ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved) : (double)x[y];
+      if (hh < G) qd[hh][j] = turn ? rotated<double>(raw[hh], j, cs, p.rope.rot, p.rope.interleaved) : (double)(float)x[y];
     }
     __syncthreads();
     if (b + 1 < b_end) fetch(b + 1);
@@ -208,18 +208,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
         key[y] = i < c.m ? min(__float_as_uint(fabsf(qt[y])), 0x7F800001u) + 1u : 0u;
         if (p.qproj_out) p.qproj_out[((size_t)b * p.Hq + (size_t)g * G + w) * D + i] = qt[y];
       }
-      // tau: the largest value with at least k keys >= tau, a bit a round from the top; the search ends when
-      // exactly k are
+      // tau: the largest value with at least k keys >= tau, two bits a round from the top, the three counts in one
+      // word; the search ends when exactly k are
       uint32_t tau = 0;
       int cnt = D;
 #pragma unroll 1
-      for (int bit = 30; bit >= 0 && cnt != p.k; --bit) {
-        const uint32_t cand = tau | (1u << bit);
-        const int n_ge = __reduce_add_sync(0xffffffffu, (int)(key[0] >= cand) + (int)(key[1] >= cand) + (int)(key[2] >= cand) +
-                                                            (int)(key[3] >= cand));
-        if (n_ge >= p.k) {
-          tau = cand;
-          cnt = n_ge;
+      for (int bit = 30; bit >= 0 && cnt != p.k; bit -= 2) {
+        const uint32_t c1 = tau | (1u << bit), c2 = tau | (2u << bit), c3 = tau | (3u << bit);
+        uint32_t n = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) n += (key[y] >= c1 ? 1u : 0u) + (key[y] >= c2 ? 0x100u : 0u) + (key[y] >= c3 ? 0x10000u : 0u);
+        n = __reduce_add_sync(0xffffffffu, n);         // each at most 128
+        const int n1 = n & 255, n2 = (n >> 8) & 255, n3 = n >> 16;
+        if (n1 >= p.k) {
+          tau = n3 >= p.k ? c3 : n2 >= p.k ? c2 : c1;
+          cnt = n3 >= p.k ? n3 : n2 >= p.k ? n2 : n1;
         }
       }
       uint32_t word[4];
@@ -262,18 +265,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
       // most half a step, so 16 times it stays in range)
       uint8_t* dst = p.qpart + ((size_t)u * NH + w) * stride * D + lane;
 #pragma unroll
-      for (int y = 0; y < 4; y += 2) {
-        float x0 = qt[y] * mul, x1 = qt[y + 1] * mul;
-        if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // an infinite query makes its scores NaN, not the largest code
-        if (!(fabsf(x1) < INFINITY)) x1 = NAN;
-        for (int i = 0; i < stride; ++i) {
-          const uint16_t code = i < parts ? f32x2_to_e4m3x2(x0, x1) : (uint16_t)0;
-          dst[i * D + 32 * y] = (uint8_t)code;
-          dst[i * D + 32 * y + 32] = (uint8_t)(code >> 8);
-          const float2 back = e4m3x2_to_f32x2(code);
-          x0 = (x0 - back.x) * 16.f;
-          x1 = (x1 - back.y) * 16.f;
-        }
+      for (int y = 0; y < 4; ++y) {
+        qt[y] *= mul;
+        if (!(fabsf(qt[y]) < INFINITY)) qt[y] = NAN;   // an infinite query makes its scores NaN, not the largest code
+      }
+#pragma unroll 1
+      for (int i = 0; i < stride; ++i, dst += D) {
+        const uint32_t code = i < parts ? f32x4_to_e4m3x4(qt[0], qt[1], qt[2], qt[3]) : 0u;
+        const float2 b0 = e4m3x2_to_f32x2((uint16_t)code), b1 = e4m3x2_to_f32x2((uint16_t)(code >> 16));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) dst[32 * y] = (uint8_t)(code >> (8 * y));
+        qt[0] = (qt[0] - b0.x) * 16.f;
+        qt[1] = (qt[1] - b0.y) * 16.f;
+        qt[2] = (qt[2] - b1.x) * 16.f;
+        qt[3] = (qt[3] - b1.y) * 16.f;
       }
     } else if (w >= 8) {
       // zeros for the heads the operand has room for but the group lacks
