@@ -272,12 +272,13 @@ def _want(t, shape, dtype, what: str) -> None:
 
 def _rows(t, heads: int, what: str) -> tuple[int, int]:
     """Element strides between the rows and between the heads of t [n, heads, d] (0: there is only one)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or not t.is_cuda:
-        raise AquaError(AQUA_ERR_ARG, f"{what} must be a device tensor [rows, {heads}, 128], not {tuple(t.shape)}")
-    row, head, one = t.stride()
-    if one != 1 or (t.shape[0] > 1 and row < 128) or (heads > 1 and head < 128):
+    shape = t.shape
+    if shape[1:] != (heads, 128) or not t.is_cuda:
+        raise AquaError(AQUA_ERR_ARG, f"{what} must be a device tensor [rows, {heads}, 128], not {tuple(shape)}")
+    n, (row, head, one) = shape[0], t.stride()
+    if one != 1 or (n > 1 and row < 128) or (heads > 1 and head < 128):
         raise AquaError(AQUA_ERR_ARG, f"{what}: rows of 128 must be dense and apart, not strides {t.stride()}")
-    return (row if t.shape[0] > 1 else 0), (head if heads > 1 else 0)
+    return (row if n > 1 else 0), (head if heads > 1 else 0)
 
 
 def _one_device(t, *others) -> int:
