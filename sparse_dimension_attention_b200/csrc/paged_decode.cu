@@ -7,9 +7,9 @@
 //
 // paged_attend_kernel, persistent: the tokens of all (b, g) are cut into tiles
 // of 128, the flat sequence of tiles into pieces.  Every block has one piece, with
-// five eighths of the work together; the rest are smaller pieces that a block
-// takes when it is done (equal shares left the slowest block 15 to 20 % behind
-// the median).  Short jobs have equal shares only.
+// five eighths of the work together; the rest are as many smaller pieces that a
+// block takes when it is done (equal shares left the slowest block 15 to 20 %
+// behind the median).  Short jobs have equal shares only.
 //
 //   s_t  = ks(page) sum_{j in U} q~_j code_t[j] / sqrt(d)
 //   w_t  = s_t log2(e) + log2 vs(page),   p_t = 2^(w_t - M),  M a lazily raised max of w
@@ -333,16 +333,21 @@ struct Cursor {
   int tile;                // tile of the unit
 };
 
+// a / b for a, b >= 0: a division of 64 bits takes several hundred cycles, one of 32 bits some tens
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The flat sequence of `total` tiles as pieces: nb first ones, then smaller ones.
 struct Pieces {
   long long total, nb;
   long long first, rest;   // tiles of a first piece and of a later one; first = 0: equal shares, nothing else
   __device__ __forceinline__ Pieces(long long t, int blocks) : total(t), nb(min((long long)blocks, t)), first(0), rest(1) {
-    // worth it from five tiles a block on: three later pieces each
+    // worth it from five tiles a block on: one later piece each (three took 59.7 us in place of 54.0 for 8192 tiles of
+    // 8 heads, a change of pieces costs 2 us; none: 52, but 216 in place of 189 for the 43000 of 32 sequences)
     if (nb > 0 && total >= 5 * nb) {
       first = total * 5 / 8 / nb;
-      const long long left = total - first * nb;
-      rest = (left + 3 * nb - 1) / (3 * nb);
+      rest = (total - first * nb + nb - 1) / nb;
     }
   }
   __device__ __forceinline__ long long start(long long p) const {
@@ -351,7 +356,7 @@ struct Pieces {
   }
   __device__ __forceinline__ int of(long long tile) const {
     if (first == 0) return (int)(((tile + 1) * nb - 1) / total);
-    return (int)(tile < nb * first ? tile / first : nb + (tile - nb * first) / rest);
+    return (int)(tile < nb * first ? quotient(tile, first) : nb + quotient(tile - nb * first, rest));
   }
   __device__ __forceinline__ int count() const {
     return (int)(first == 0 ? nb : nb + (total - nb * first + rest - 1) / rest);
@@ -374,6 +379,7 @@ struct AttendMisc {
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t drain;
   TileInfo info[kVStages];
+  int pid[kVStages][TT / 16];      // its pages, one every 16 tokens; -1: none
   int stop[2];                     // softmax threads leave after this (even, odd) tile
   float ks[kVStages][TT / 16];     // key scale of every 16 tokens; negative: their page does not exist
   float vs[kVStages][TT / 16];
@@ -383,6 +389,8 @@ struct AttendMisc {
   uint32_t tmem;
   int abort;
 };
+
+static_assert(sizeof(AttendMisc) <= 1024, "two blocks an SM: 113 KB each, 112 of them tiles and operands");
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;
@@ -623,11 +631,11 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
 
-  // page of 16 tokens of a tile, chunk `lane` (lanes 0..7 of a copying warp)
+  // pages of the 512 tokens from a tile on, 16 tokens a lane
   auto page_of_chunk = [&](int b, int tile, int len) {
     int pid = -1;
     const int t = tile * TT + 16 * lane;
-    if (lane < TT / 16 && t < len) {
+    if (t < len) {
       pid = __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2));
       if (pid < 0 || pid >= c.n_pages) {
         pid = -1;
@@ -641,9 +649,9 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   if (w >= kKeyWarp0) {
     // ================= key rows, scales, queries =================
     const int ct = tid - kKeyWarp0 * 32, lc = ct & 7, lr = ct >> 3;    // chunk of 16 tokens, first row (dim)
-    auto copy_keys = [&](int t, const TileInfo& ti, int mypid, const uint4& um) {
+    auto copy_keys = [&](int t, const TileInfo& ti, const uint4& um) {
       const uint32_t kbase = smem0 + off_k + (t % kKStages) * mrows * TT;
-      const int pid = __shfl_sync(0xffffffffu, mypid, lc);
+      const int pid = ms.pid[t % kVStages][lc];
       // rows lr, lr + 16, ...; rows that are not wanted are zeros
       const uint8_t* kb = c.k;
       if (pid >= 0) kb += c.kblock(pid, ti.g) + ((ti.tile * TT + 16 * lc) & pmask) + ((size_t)lr << c.page_log2);
@@ -690,14 +698,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     auto low = [&](int wd) { return c.m >= 32 * wd + 32 ? f : (c.m > 32 * wd ? (1u << (c.m - 32 * wd)) - 1u : 0u); };
     const uint4 all = make_uint4(low(0), low(1), low(2), low(3));
     TileInfo ti = info_of(0);
-    int mypid = page_of_chunk(ti.b, ti.tile, ti.len);
-    copy_keys(0, ti, mypid, all);
+    copy_keys(0, ti, all);
     const bool two = !(ti.flags & kEnd);
     TileInfo tn = ti;
     if (two) {
       tn = info_of(1);
-      mypid = page_of_chunk(tn.b, tn.tile, tn.len);
-      copy_keys(1, tn, mypid, all);
+      copy_keys(1, tn, all);
     }
     pdl_wait();                               // the selection's results
     finish(0, ti);
@@ -707,14 +713,13 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     for (int t = 2; two && !(tn.flags & kEnd); ++t) {
       tn = info_of(t);
       if (__any_sync(0xffffffffu, *(volatile int*)&ms.abort)) break;      // (no barrier among these warps)
-      mypid = page_of_chunk(tn.b, tn.tile, tn.len);
       if (tn.u != iu) {
         iu = tn.u;
         um = p.umask[iu];
       }
       wait_or_abort(&ms.k_empty[t % kKStages], ((t / kKStages) - 1) & 1, &ms.abort, p.ctrl);
       __syncwarp();
-      copy_keys(t, tn, mypid, um);
+      copy_keys(t, tn, um);
       finish(t, tn);
     }
     cp_async_wait_all();
@@ -729,14 +734,21 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     int iu = -1, ord = -1;
     bool part_first = true, waited = false;    // the piece's first tile is next; the earlier kernels' results may be read
     int seg_first = 0;                         // first tile of the unit in this piece
+    int4 split = make_int4(0, 0, 0, 0);
+    int split_at = -1;
     // A piece that is the second of a unit's pieces puts the unit on the list of the merge.
     auto note_split = [&]() {
       if (cur.tile == 0) return;
       const long long f = begin - cur.tile;                   // the unit's tiles are [f, f + n)
       const int first = pieces.of(f);
       if (first != piece - 1) return;
-      p.split[atomicAdd(p.ctl + 1, 1)] =
-          make_int4(cur.u, first, pieces.of(f + n_tiles(cur.len) - 1), pieces.start(first) < f ? 1 : 0);
+      split = make_int4(cur.u, first, pieces.of(f + n_tiles(cur.len) - 1), pieces.start(first) < f ? 1 : 0);
+      split_at = atomicAdd(p.ctl + 1, 1);
+    };
+    // (the entry is stored a little later, when its place is known without a wait)
+    auto store_split = [&]() {
+      if (split_at >= 0) p.split[split_at] = split;
+      split_at = -1;
     };
     // The first value rows come while the selection runs; then its results, and the merge of an earlier call, which
     // has read its parts.
@@ -752,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
       }
     };
     int next_piece = -1;
-    int mypid = page_of_chunk(cur.b, cur.tile, cur.len);
+    // pages of the four tiles from `base` of unit `base_u` on, eight lanes a tile
+    int base = cur.tile, base_u = cur.u, pids = page_of_chunk(cur.b, cur.tile, cur.len);
     for (int t = 0;; ++t) {
       const int st = t % kVStages;
       if (!waited && (t >= kVStages || (more && left <= 3))) after_wait();
@@ -774,6 +787,10 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         part_first = false;
         seg_first = cur.tile;
       }
+      int mypid = __shfl_sync(0xffffffffu, pids, 8 * (cur.tile - base) + (lane & 7));
+      if (lane >= TT / 16) mypid = -1;
+      if (lane < TT / 16) ms.pid[st][lane] = mypid;
+      __syncwarp();
       if (lane == 0) {
         const bool unit_end = cur.tile + 1 == n_tiles(cur.len);
         TileInfo ti;
@@ -793,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
       __syncwarp();
       if (go)
         tma_rows(smem0 + st * kStageV + 16 * lane * D, &vmap, (mypid * c.Hkv + cur.g) << c.page_log2, &ms.v_full[st]);
+      store_split();
       if (end) break;
       if (--left > 0) {
         next_tile(c, p, cur);
@@ -802,28 +820,35 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         begin = pieces.start(piece);
         stop_at = pieces.start(piece + 1);
         left = (int)(stop_at - begin);
-        const int want = (int)(begin / c.Hkv);
-        int lo = 0, hi = c.B;                  // prefix[lo] <= want < prefix[hi]
-        while (hi - lo > 1) {
+        const int want = (int)quotient(begin, c.Hkv);
+        int lo = 0, hi = c.B, before, len;     // prefix[lo] <= want < prefix[hi]
+        do {
           const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-          const bool under = at < hi && __ldcg(p.prefix + at) <= want;
-          const int k = 31 - __clz(__ballot_sync(0xffffffffu, under));     // lane 0 is always under
+          const int tiles = at < hi ? __ldcg(p.prefix + at) : 0x7fffffff, tokens = at < hi ? seq_tokens(c, p, at) : 0;
+          const int k = 31 - __clz(__ballot_sync(0xffffffffu, at < hi && tiles <= want));   // lane 0 is always under
+          before = __shfl_sync(0xffffffffu, tiles, k);
+          len = __shfl_sync(0xffffffffu, tokens, k);
           hi = min(hi, lo + (k + 1) * step);
           lo += k * step;
-        }
+        } while (hi - lo > 1);
         // sequences without tiles share their prefix with the next one: lo is the last of them, which has tiles
         cur.b = lo;
-        cur.len = seq_tokens(c, p, lo);
-        const int x = n_tiles(cur.len), r = (int)(begin - (long long)__ldcg(p.prefix + lo) * c.Hkv);
+        cur.len = len;
+        const int x = n_tiles(len), r = (int)(begin - (long long)before * c.Hkv);
         cur.g = r / x;
         cur.tile = r % x;
         cur.u = lo * c.Hkv + cur.g;
         part_first = true;
-        if (lane == 0) note_split();
       }
-      mypid = page_of_chunk(cur.b, cur.tile, cur.len);
+      if (cur.u != base_u || (unsigned)(cur.tile - base) >= 4u) {
+        base = cur.tile;
+        base_u = cur.u;
+        pids = page_of_chunk(cur.b, cur.tile, cur.len);
+      }
+      if (part_first && lane == 0) note_split();
     }
     if (!waited) after_wait();
+    store_split();
   } else if (w == kMmaWarp) {
     // ================= products =================
     if (lane == 0) {
@@ -1059,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 constexpr int kMergeWarps = 8;
 constexpr int kMaxPieces = 2048;
 constexpr int kMergeFew = 8;
-constexpr int kPiecesPerBlock = 4;         // one first piece and three later ones
+constexpr int kPiecesPerBlock = 2;         // a first piece and a later one
 
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
   __shared__ __align__(16) float sum[kMergeWarps][D];
