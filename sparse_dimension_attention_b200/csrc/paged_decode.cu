@@ -383,8 +383,11 @@ struct AttendMisc {
   int stop[2];                     // softmax threads leave after this (even, odd) tile
   float ks[kVStages][TT / 16];     // key scale of every 16 tokens; negative: their page does not exist
   float vs[kVStages][TT / 16];
-  float red[4][kMaxG];
-  long long scan[kThreads / 32];
+  float fac[kVStages][kMaxG];      // factors of a unit's queries, at its first tile
+  union {
+    float red[4][kMaxG];
+    long long scan[kThreads / 32];          // before the roles begin
+  };
   Cursor cur;
   uint32_t tmem;
   int abort;
@@ -683,6 +686,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           const int r = i >> 3, ch = i & 7;
           cp_async16_zfill(qbase + r * D + ((ch ^ (r & 7)) << 4), p.qpart + ((size_t)ti.u * N + r) * D + ch * 16, true);
         }
+        // (a tile's slot, not the unit's: the softmax has read it when the tile's value buffer is free again)
+        if (ct < G) cp_async_small<4>(&ms.fac[t % kVStages][ct], p.qfac + (size_t)ti.u * kMaxG + ct);
       }
       // the copies arrive when they have landed; the product warp makes them visible to the tensor cores
       cp_async_arrive_noinc(&ms.k_full[t % kKStages]);
@@ -923,13 +928,16 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         begun = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          fac[h] = h < G ? p.qfac[(size_t)ti.u * kMaxG + h] : 0.f;
           ref[h] = -INFINITY;
           l[h] = 0.f;
         }
       }
       wait(&ms.s_full[buf], (t >> 1) & 1);    // and the scales have landed, before the scores were issued
       tc_fence_after();
+      if (ti.flags & kFirst) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) fac[h] = h < G ? ms.fac[st][h] : 0.f;
+      }
       const float ksc = ms.ks[st][tid >> 4], vsc = ms.vs[st][tid >> 4];
       const bool seen = ksc >= 0.f && ti.tile * TT + tid < ti.len;
       const float lv = __log2f(vsc), iv = 1.f / vsc;
