@@ -352,9 +352,17 @@ AQUA_API int aqua_selftest_wait_timeout(aqua_cache* cache, unsigned long long li
  *   d       128;  1 <= d_store <= d (d_store < d: AQUA-Memory on the keys)
  *   page_size  16, 32, 64 or 128 tokens
  *   dtype   AQUA_E4M3
+ *   limits  Hkv <= 65535, B * Hkv <= 2^24, n_pages * Hkv * page_size < 2^31 (256 GB of
+ *           values), max_pages * page_size <= 2^30, B times that <= 2^37
+ *           (AQUA_ERR_UNSUPPORTED beyond)
  *
  * A page that aqua_paged_append writes must appear once in the table and in one
  * sequence only; full pages that are only read may be shared (prefixes).
+ *
+ * aqua_paged_append and aqua_paged_decode_attn read P before they wait for the
+ * preceding kernel on the stream (everything else only after it), which is safe
+ * unless the kernel that wrote P released its dependents early through
+ * programmatic dependent launch (no kernel here that writes it does).
  *
  * Device data that the host cannot check is checked by the kernels, which then
  * record AQUA_ERR_ARG in the status word and touch nothing out of bounds: a
@@ -414,9 +422,10 @@ AQUA_API int aqua_paged_status(const aqua_paged_cache* cache, int* status_out, a
  * Appending a run at once or token by token gives the same values but for those
  * subnormals and for sums within f32 rounding of a tie: single tokens are
  * projected in f64, short runs in f32, long ones on the tensor cores with both
- * factors in two f16 parts, which is as exact as an f32 sum.  A sequence whose run does not fit (or lies outside the rotation
- * table, or whose cu_new is not ascending within [0, n_tokens]) is left as it
- * was and AQUA_ERR_ARG recorded.
+ * factors in two f16 parts, which is as exact as an f32 sum.
+ * A sequence whose run does not fit (or lies outside the rotation table, or
+ * whose cu_new is not ascending within [0, n_tokens]) is left as it was and
+ * AQUA_ERR_ARG recorded.
  */
 AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new, const void* v_new, int io_dtype,
                                long long k_stride, long long k_head_stride, long long v_stride,
@@ -440,9 +449,10 @@ AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new,
  *              bytes, no initialisation.  Calls that may overlap on the GPU need
  *              a workspace each.
  * Hq a multiple of Hkv with Hq / Hkv in 1 .. 8.  A sequence of length 0 gets a
- * zero output and lse = -inf.  Scores, softmax statistics and sums are f32;
- * queries and probabilities enter the tensor cores as two f16 parts (about 22
- * bits), codes exactly.
+ * zero output and lse = -inf.  Scores, softmax statistics and sums are f32.
+ * Codes enter the tensor cores as they are, queries and probabilities as sums
+ * of e4m3 parts: 15 and 11 bits or more for a bf16 output, about 24 for an f32
+ * one.  A query with an infinity or NaN among its kept dimensions gives NaN.
  */
 AQUA_API size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq);
 AQUA_API int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,

@@ -48,6 +48,9 @@ int validate(const aqua_paged_cache* c) {
   // slots of a sequence are counted in 32 bits
   if ((long long)c->max_pages * c->page_size > (1LL << 30))
     return set_error(AQUA_ERR_UNSUPPORTED, "paged cache: max_pages * page_size over 2^30 tokens");
+  // tiles of 128 tokens of all sequences are counted in 32 bits
+  if ((long long)c->max_pages * c->page_size > (1LL << 37) / c->B)
+    return set_error(AQUA_ERR_UNSUPPORTED, "paged cache: B * max_pages * page_size over 2^37 tokens");
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16))
     return set_error(AQUA_ERR_ARG, "paged cache: pages must be 16-byte aligned");
   if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->block_table, 4) || !aligned(c->ctrl, 4))
@@ -104,6 +107,16 @@ aqua::PagedView view_of(const aqua_paged_cache* c) {
   return v;
 }
 
+// No exception (host memory, a mutex) leaves a C entry point.
+template <typename F>
+int guarded(const char* who, F launch) noexcept {
+  try {
+    return launch();
+  } catch (...) {
+    return set_error(AQUA_ERR_CUDA, "%s: out of host resources", who);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -138,8 +151,10 @@ int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new, const vo
   if (n_tokens < 1) return set_error(AQUA_ERR_ARG, "%s: n_tokens=%d", who, n_tokens);
   if (cu_new == nullptr && n_tokens != cache->B)
     return set_error(AQUA_ERR_ARG, "%s: n_tokens=%d without cu_new, but B=%d", who, n_tokens, cache->B);
-  return aqua::launch_paged_append(view_of(cache), k_new, v_new, io_dtype == AQUA_BF16, ks, vs, n_tokens, start,
-                                   cu_new, P, rv, reinterpret_cast<cudaStream_t>(stream));
+  return guarded(who, [&] {
+    return aqua::launch_paged_append(view_of(cache), k_new, v_new, io_dtype == AQUA_BF16, ks, vs, n_tokens, start,
+                                     cu_new, P, rv, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq) {
@@ -177,9 +192,11 @@ int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, co
   if (workspace_bytes < need)
     return set_error(AQUA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
   if (!(scale > 0.f)) scale = 1.0f / std::sqrt((float)cache->d);
-  return aqua::launch_paged_decode(view_of(cache), len, q, io_dtype == AQUA_BF16, qs, P, rv, Hq, k, scale, out,
-                                   out_dtype == AQUA_BF16, sel_out, qproj_out, lse_out, workspace,
-                                   reinterpret_cast<cudaStream_t>(stream));
+  return guarded(who, [&] {
+    return aqua::launch_paged_decode(view_of(cache), len, q, io_dtype == AQUA_BF16, qs, P, rv, Hq, k, scale, out,
+                                     out_dtype == AQUA_BF16, sel_out, qproj_out, lse_out, workspace,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 int aqua_paged_gather(const aqua_paged_cache* cache, const int32_t* len, const int32_t* seq_idx, aqua_cache* dst,
@@ -206,7 +223,9 @@ int aqua_paged_gather(const aqua_paged_cache* cache, const int32_t* len, const i
                      dst->Tcap);
   if (!aligned(dst->k_proj, 16) || !aligned(dst->v, 16))
     return set_error(AQUA_ERR_ARG, "%s: dst k_proj and v must be 16-byte aligned", who);
-  rc = aqua::launch_paged_gather(view_of(cache), len, seq_idx, dst, max_len, reinterpret_cast<cudaStream_t>(stream));
+  rc = guarded(who, [&] {
+    return aqua::launch_paged_gather(view_of(cache), len, seq_idx, dst, max_len, reinterpret_cast<cudaStream_t>(stream));
+  });
   if (rc == AQUA_OK) dst->max_len = max_len;
   return rc;
 }

@@ -230,3 +230,28 @@ def test_python_layer_refuses_what_c_cannot_see():
     rope = aq.AquaRope.from_theta(16, rot_dim=32, device="cpu")
     assert rope.desc.n_pos == 16 and rope.desc.rot_dim == 32
     np.testing.assert_allclose(rope.cos_sin[3, 0].item(), np.cos(3.0), rtol=1e-7)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_pages=1 << 24, Hkv=2),                                      # 2^31 value rows with pages of 64
+    dict(n_pages=(1 << 31) - 1, Hkv=8),
+    dict(Hkv=65536, B=1), dict(B=1 << 23, Hkv=4),
+    dict(max_pages=(1 << 24) + 1),                                     # over 2^30 slots a sequence
+    dict(B=1 << 20, max_pages=(1 << 11) + 1),                          # over 2^37 slots of all sequences
+    dict(B=(1 << 24) - 1, Hkv=1, max_pages=(1 << 24)),
+])
+def test_sizes_past_the_counters_are_refused(lib, kw):
+    """Rows, slots and tiles are counted in 32 bits on the device: nothing is launched past that."""
+    c = _desc(**kw)
+    assert _append(lib, c, n=c.B) == abi.AQUA_ERR_UNSUPPORTED
+    assert _decode(lib, c, Hq=c.Hkv) == abi.AQUA_ERR_UNSUPPORTED
+    assert lib.aqua_paged_decode_workspace_size(ctypes.byref(c), c.Hkv) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_pages=(1 << 24) - 1, Hkv=2), dict(max_pages=1 << 24), dict(B=1 << 20, max_pages=1 << 11),
+])
+def test_the_largest_sizes_are_accepted(lib, kw):
+    c = _desc(**kw)
+    assert lib.aqua_paged_decode_workspace_size(ctypes.byref(c), 8) > 0
+    assert _append(lib, c, n=0) == abi.AQUA_ERR_ARG                    # the cache passed; the count did not
