@@ -2,7 +2,8 @@
 // times its page's scale, keys dimension-major, values token-major.
 //
 // A copy bound by memory: (m + 128) bytes read and 2 or 4 times that written for
-// each token and head.
+// each token and head.  16 ragged sequences of up to 16384 tokens, 8 heads, to bf16:
+// 122 us against 106 at the copy rate (87 %).
 #include "paged_internal.cuh"
 
 namespace aqua {
