@@ -883,3 +883,80 @@ def test_prompt_then_decode_steps():
         got = run_paged_decode(cache, qn, lens, Pt, k, rope, torch.bfloat16, torch.bfloat16)
         check_decode(got, oracle_decode(snap(cache), lens, qn, P32, k, rn, inter, "bf16"), lens, k, m, True)
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,m,k,longest", [(1100, 4, 1, 32, 20, 400), (90, 64, 8, 128, 70, 1500)])
+def test_decode_large_batches_with_shared_prefixes(B, Hq, Hkv, m, k, longest):
+    """Several sequences a selection block, a search for a piece's sequence of several rounds, later pieces; the
+    first pages of half of the sequences are the same ones, some sequences are empty."""
+    rng = np.random.default_rng(50)
+    page = 16
+    lens = [int(x) for x in rng.integers(0, longest, B)]
+    lens[7], lens[B - 1] = 0, 0
+    _, P32 = calib_P(Hkv)
+    cache = make_cache(B, Hkv, page, m, longest // page + 1, seed=51)
+    cache.block_table[::2, :3] = cache.block_table[0, :3].clone()
+    q = tdev(rows_of(rng, B, Hq, "f32", 0.3))
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, Hq),), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = []
+    for _ in range(2):
+        out = torch.empty(B, Hq, 128, device="cuda")
+        aq.aqua_paged_decode_attn(cache.desc, q, lt, tdev(P32), Hq, k, out, ws)
+        outs.append(out)
+    ref = torch_decode(cache, q, lens, tdev(P32), k)
+    live = lt > 0
+    assert float(((outs[0].double() - ref).norm(dim=-1)[live] / ref.norm(dim=-1)[live]).max()) <= 1e-5
+    assert bool((outs[0][~live] == 0).all()) and torch.equal(outs[0], outs[1])
+    assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+def test_captured_appends_and_gathers_on_other_streams():
+    """Runs long enough for the tensor cores, captured on a stream of their own with the gather after them and
+    replayed with other lengths; then appends to two caches at once on two streams.  The same bytes as calls of
+    their own."""
+    rng = np.random.default_rng(60)
+    Hkv, page, m, B, cap = 8, 64, 96, 3, 1024
+    _, P32 = calib_P(Hkv)
+    Pt = tdev(P32)
+    rope, _, _ = rope_of((128, False), cap)
+    N = 1500
+    k = tdev(rows_of(rng, N, Hkv, "bf16"), torch.bfloat16)
+    v = tdev(rows_of(rng, N, Hkv, "bf16"), torch.bfloat16)
+    one, two = make_cache(B, Hkv, page, m, cap // page, seed=61), make_cache(B, Hkv, page, m, cap // page, seed=61)
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ln = torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 0, 0, N], dtype=torch.int32, device="cuda")
+    dst, ref_dst = aq.AquaCache(2, Hkv, cap, d_store=m), aq.AquaCache(2, Hkv, cap, d_store=m)
+    idx = torch.tensor([2, 2], dtype=torch.int32, device="cuda")
+    def step(cache, d, stream=None):
+        aq.aqua_paged_append(cache.desc, k, v, start, Pt, cu_new=cu, rope=rope, stream=stream)
+        aq.aqua_paged_gather(cache.desc, ln, d.desc, cap, seq_idx=idx, stream=stream)
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        step(one, dst)
+    for starts, cuts in (([5, 300, 0], [0, 600, 700, 1500]), ([605, 400, 0], [0, 0, 601, 1500]), ([0, 0, 100], [0, 500, 700, 1500])):
+        start.copy_(torch.tensor(starts, dtype=torch.int32))
+        cu.copy_(torch.tensor(cuts, dtype=torch.int32))
+        ln.copy_(start + cu[1:] - cu[:-1])
+        g.replay()
+        step(two, ref_dst)
+        torch.cuda.synchronize()
+        a, b = snap(one), snap(two)
+        for n in a:
+            np.testing.assert_array_equal(a[n], b[n], err_msg=n)
+        n = int(ln[2])
+        for x, y in ((dst.k_proj[..., :n], ref_dst.k_proj[..., :n]), (dst.v[:, :, :n], ref_dst.v[:, :, :n])):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+        assert torch.equal(dst.v[0, :, :n].view(torch.int16), dst.v[1, :, :n].view(torch.int16))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s, c in zip(streams, (one, two)):
+        aq.aqua_paged_append(c.desc, k, v, start, Pt, cu_new=cu, rope=rope, stream=s)
+        aq.aqua_paged_append(c.desc, k[:B], v[:B], ln, Pt, rope=rope, stream=s)
+    torch.cuda.synchronize()
+    a, b = snap(one), snap(two)
+    for n in a:
+        np.testing.assert_array_equal(a[n], b[n], err_msg=n)
+    assert aq.aqua_paged_status(one.desc) == aq.AQUA_OK and aq.aqua_paged_status(two.desc) == aq.AQUA_OK
