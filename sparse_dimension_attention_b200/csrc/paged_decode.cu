@@ -1247,12 +1247,12 @@ int attend_blocks(int per_sm) {
 
 template <typename T>
 int launch_select(const PagedView& c, const DecodeP& p, int G, int NH, int stride, int parts, cudaStream_t st) {
-  // As many sequences a block as leave one block an SM: P is read once for all of them, and an attention block
-  // fits beside it and fetches its first tiles.  (256 units, two blocks an SM: selection 10 us, attention from 11 us.)
-  // With three sequences a block or more the selection itself is what takes long, and two blocks an SM overlap
-  // (1560 units of 8 heads: 78 us in one block an SM, 57 in two).
+  // As many sequences a block as leave one or two blocks an SM: P is read once for all of them, and where there is
+  // one, an attention block fits beside it and fetches its first tiles.
+  // With two sequences a block or more the selection itself is what takes long, and two blocks an SM overlap
+  // (1560 units of 8 heads: 78 us in one block an SM, 57 in two; a step of 256 units of 4 heads: 41.2 and 39.0).
   const int sms = device_sm_count();
-  const int waves = (long long)c.B * c.Hkv > 2 * sms ? 2 : 1;
+  const int waves = (long long)c.B * c.Hkv > sms ? 2 : 1;
   const int each = waves * sms / c.Hkv > 0 ? waves * sms / c.Hkv : 1;                 // blocks a head
   const int group = (c.B + each - 1) / each;
   const dim3 grid((c.B + group - 1) / group, c.Hkv);
