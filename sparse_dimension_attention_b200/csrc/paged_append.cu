@@ -167,13 +167,12 @@ __device__ __forceinline__ float page_scale(float amax, float old, int fill) {
   return fill > 0 ? fmaxf(old, s) : s;
 }
 
-// One block per (page segment, KV head).  A thread holds 16 rows x 4 columns of P
-// in registers for the whole segment, so P is read once; eight tokens at a time
-// are projected (warp w sums input dims 16w .. 16w+15) and their eight partial
-// sums added in order.  Bound by the reads of the rows from shared memory, 0.3 us a
-// token and block.
+// A block takes page segments of one KV head.  A thread holds 16 rows x 4 columns of
+// P in registers, so P is read once; eight tokens at a time are projected (warp w
+// sums input dims 16w .. 16w+15) and their eight partial sums added in order.
+// Bound by the reads of the rows from shared memory, 0.3 us a token and block.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c, AppendParams a) {
+__global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c, AppendParams a, int segs) {
   extern __shared__ __align__(16) float dyn[];
   float* kt = dyn;                                         // [page][D] projected keys
   float* part = kt + ((size_t)D << c.page_log2);           // [kWarps][kGroup][D]
@@ -181,102 +180,106 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
   float* raw = xs + kGroup * D;
   __shared__ float red[2][kWarps];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-  Segment s;
-  if (!find_segment(a, c, blockIdx.x, s)) return;
-  const int pid = __ldg(c.table + (size_t)s.b * c.max_pages + (s.slot >> c.page_log2));
-  if (pid < 0 || pid >= c.n_pages) {
-    if (threadIdx.x == 0) report_arg(c);
-    return;
-  }
-  const T* kr = static_cast<const T*>(a.k_new) + (size_t)s.token * a.ks.row + (size_t)h * a.ks.head;
-  const T* vr = static_cast<const T*>(a.v_new) + (size_t)s.token * a.vs.row + (size_t)h * a.vs.head;
   float4 p[kRows];
   const float4* Pg = reinterpret_cast<const float4*>(a.P + (size_t)h * D * D);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) p[i] = __ldg(Pg + (w * kRows + i) * (D / 4) + lane);
+#pragma unroll 1
+  for (int seg = blockIdx.x; seg < segs; seg += gridDim.x) {
+    __syncthreads();                         // the search's shared words are free again
+    Segment s;
+    if (!find_segment(a, c, seg, s)) return;
+    const int pid = __ldg(c.table + (size_t)s.b * c.max_pages + (s.slot >> c.page_log2));
+    if (pid < 0 || pid >= c.n_pages) {
+      if (threadIdx.x == 0) report_arg(c);
+      continue;
+    }
+    const T* kr = static_cast<const T*>(a.k_new) + (size_t)s.token * a.ks.row + (size_t)h * a.ks.head;
+    const T* vr = static_cast<const T*>(a.v_new) + (size_t)s.token * a.vs.row + (size_t)h * a.vs.head;
 
-  float kmax = 0.f, vmax = 0.f;
-  for (int t0 = 0; t0 < s.n; t0 += kGroup) {
-    const int nt = min(kGroup, s.n - t0);
-    if (w < nt) {
+    float kmax = 0.f, vmax = 0.f;
+    for (int t0 = 0; t0 < s.n; t0 += kGroup) {
+      const int nt = min(kGroup, s.n - t0);
+      if (w < nt) {
+        float f[4];
+        load4<T>(kr + (size_t)(t0 + w) * a.ks.row + 4 * lane, f);
+        *reinterpret_cast<float4*>(raw + w * D + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
+        __syncwarp();
+        if (a.rope.cs != nullptr) {
+          const float* cs = a.rope.cs + (size_t)(s.slot + t0 + w) * a.rope.rot;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = rotated<float>(raw + w * D, 4 * lane + e, cs, a.rope.rot, a.rope.interleaved);
+        }
+        *reinterpret_cast<float4*>(xs + w * D + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
+        load4<T>(vr + (size_t)(t0 + w) * a.vs.row + 4 * lane, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vmax = fmaxf(vmax, finite_abs(f[e]));
+      }
+      __syncthreads();
+      for (int t = 0; t < nt; ++t) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const float x = xs[t * D + w * kRows + i];
+          acc.x = fmaf(x, p[i].x, acc.x); acc.y = fmaf(x, p[i].y, acc.y);
+          acc.z = fmaf(x, p[i].z, acc.z); acc.w = fmaf(x, p[i].w, acc.w);
+        }
+        *reinterpret_cast<float4*>(part + (w * kGroup + t) * D + 4 * lane) = acc;
+      }
+      __syncthreads();
+      if (w < nt) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float4 q = *reinterpret_cast<const float4*>(part + (x * kGroup + w) * D + 4 * lane);
+          y[0] += q.x; y[1] += q.y; y[2] += q.z; y[3] += q.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * lane + e < c.m) kmax = fmaxf(kmax, finite_abs(y[e]));
+        *reinterpret_cast<float4*>(kt + (size_t)(t0 + w) * D + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+    }
+    if (lane == 0) {
+      red[0][w] = kmax;
+      red[1][w] = vmax;
+    }
+    __syncthreads();
+    for (int x = 0; x < kWarps; ++x) {
+      kmax = fmaxf(kmax, red[0][x]);
+      vmax = fmaxf(vmax, red[1][x]);
+    }
+    const int fill = s.slot & ((1 << c.page_log2) - 1);
+    const size_t si = (size_t)pid * c.Hkv + h;
+    const float kold = c.ks[si], vold = c.vs[si];
+    const float ks = page_scale(kmax, kold, fill), vs = page_scale(vmax, vold, fill);
+    uint8_t* kb = c.k + c.kblock(pid, h);
+    uint8_t* vb = c.v + c.vblock(pid, h);
+    if (fill > 0 && ks != kold) recode_keys(kb, c.m, c.page_log2, fill, kold / ks, threadIdx.x, kThreads);
+    if (fill > 0 && vs != vold) recode_values(vb, fill, vold / vs, threadIdx.x, kThreads);
+    __syncthreads();                         // everybody has read the old scales; old codes are in place
+    if (threadIdx.x == 0) {
+      c.ks[si] = ks;
+      c.vs[si] = vs;
+    }
+    const float ki = 1.f / ks, vi = 1.f / vs;
+    // keys: one byte per (dimension, slot), consecutive threads on consecutive slots
+    for (int i = threadIdx.x; i < c.m * s.n; i += kThreads) {
+      const int j = i / s.n, t = i - j * s.n;
+      kb[((size_t)j << c.page_log2) + fill + t] = (uint8_t)f32x2_to_e4m3x2(kt[(size_t)t * D + j] * ki, 0.f);
+    }
+    for (int t = w; t < s.n; t += kWarps) {
       float f[4];
-      load4<T>(kr + (size_t)(t0 + w) * a.ks.row + 4 * lane, f);
-      *reinterpret_cast<float4*>(raw + w * D + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
-      __syncwarp();
-      if (a.rope.cs != nullptr) {
-        const float* cs = a.rope.cs + (size_t)(s.slot + t0 + w) * a.rope.rot;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = rotated<float>(raw + w * D, 4 * lane + e, cs, a.rope.rot, a.rope.interleaved);
-      }
-      *reinterpret_cast<float4*>(xs + w * D + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
-      load4<T>(vr + (size_t)(t0 + w) * a.vs.row + 4 * lane, f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) vmax = fmaxf(vmax, finite_abs(f[e]));
+      load4<T>(vr + (size_t)t * a.vs.row + 4 * lane, f);
+      reinterpret_cast<uint32_t*>(vb + (size_t)(fill + t) * D)[lane] =
+          f32x4_to_e4m3x4(f[0] * vi, f[1] * vi, f[2] * vi, f[3] * vi);
     }
-    __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float x = xs[t * D + w * kRows + i];
-        acc.x = fmaf(x, p[i].x, acc.x); acc.y = fmaf(x, p[i].y, acc.y);
-        acc.z = fmaf(x, p[i].z, acc.z); acc.w = fmaf(x, p[i].w, acc.w);
-      }
-      *reinterpret_cast<float4*>(part + (w * kGroup + t) * D + 4 * lane) = acc;
-    }
-    __syncthreads();
-    if (w < nt) {
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        const float4 q = *reinterpret_cast<const float4*>(part + (x * kGroup + w) * D + 4 * lane);
-        y[0] += q.x; y[1] += q.y; y[2] += q.z; y[3] += q.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * lane + e < c.m) kmax = fmaxf(kmax, finite_abs(y[e]));
-      *reinterpret_cast<float4*>(kt + (size_t)(t0 + w) * D + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
-    vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-  }
-  if (lane == 0) {
-    red[0][w] = kmax;
-    red[1][w] = vmax;
-  }
-  __syncthreads();
-  for (int x = 0; x < kWarps; ++x) {
-    kmax = fmaxf(kmax, red[0][x]);
-    vmax = fmaxf(vmax, red[1][x]);
-  }
-  const int fill = s.slot & ((1 << c.page_log2) - 1);
-  const size_t si = (size_t)pid * c.Hkv + h;
-  const float kold = c.ks[si], vold = c.vs[si];
-  const float ks = page_scale(kmax, kold, fill), vs = page_scale(vmax, vold, fill);
-  uint8_t* kb = c.k + c.kblock(pid, h);
-  uint8_t* vb = c.v + c.vblock(pid, h);
-  if (fill > 0 && ks != kold) recode_keys(kb, c.m, c.page_log2, fill, kold / ks, threadIdx.x, kThreads);
-  if (fill > 0 && vs != vold) recode_values(vb, fill, vold / vs, threadIdx.x, kThreads);
-  __syncthreads();                         // everybody has read the old scales; old codes are in place
-  if (threadIdx.x == 0) {
-    c.ks[si] = ks;
-    c.vs[si] = vs;
-  }
-  const float ki = 1.f / ks, vi = 1.f / vs;
-  // keys: one byte per (dimension, slot), consecutive threads on consecutive slots
-  for (int i = threadIdx.x; i < c.m * s.n; i += kThreads) {
-    const int j = i / s.n, t = i - j * s.n;
-    kb[((size_t)j << c.page_log2) + fill + t] = (uint8_t)f32x2_to_e4m3x2(kt[(size_t)t * D + j] * ki, 0.f);
-  }
-  for (int t = w; t < s.n; t += kWarps) {
-    float f[4];
-    load4<T>(vr + (size_t)t * a.vs.row + 4 * lane, f);
-    reinterpret_cast<uint32_t*>(vb + (size_t)(fill + t) * D)[lane] =
-        f32x4_to_e4m3x4(f[0] * vi, f[1] * vi, f[2] * vi, f[3] * vi);
   }
 }
 
@@ -1106,8 +1109,10 @@ int launch_run(const PagedView& c, const AppendParams& a, cudaStream_t st) {
   if (rc != AQUA_OK) return rc;
   // a run of n >= 1 tokens touches at most (n - 2) / page + 2 pages, and at most n
   const long long by_page = a.n_tokens / (1 << c.page_log2) + 2LL * c.B;
-  const unsigned segs = (unsigned)(by_page < a.n_tokens ? by_page : a.n_tokens);
-  paged_append_run_kernel<T><<<dim3(segs, c.Hkv), kThreads, smem, st>>>(c, a);
+  const int segs = (int)(by_page < a.n_tokens ? by_page : a.n_tokens);
+  // no more blocks than run at once, two an SM: each reads P once (304 segments of 16 heads: 49 us with a block each)
+  const int each = 2 * device_sm_count() / c.Hkv > 0 ? 2 * device_sm_count() / c.Hkv : 1;
+  paged_append_run_kernel<T><<<dim3(segs < each ? segs : each, c.Hkv), kThreads, smem, st>>>(c, a, segs);
   return check_launch("paged_append_run_kernel");
 }
 

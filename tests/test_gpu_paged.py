@@ -960,3 +960,27 @@ def test_captured_appends_and_gathers_on_other_streams():
     for n in a:
         np.testing.assert_array_equal(a[n], b[n], err_msg=n)
     assert aq.aqua_paged_status(one.desc) == aq.AQUA_OK and aq.aqua_paged_status(two.desc) == aq.AQUA_OK
+
+
+def test_append_short_runs_of_many_sequences():
+    """More page segments than blocks: a block takes several, one of them on a page that does not exist."""
+    rng = np.random.default_rng(70)
+    B, Hkv, page, m = 350, 2, 16, 48
+    n = [int(x) for x in rng.integers(0, 5, B)]
+    start = [int(x) for x in rng.integers(0, 40, B)]
+    n[9], start[9], n[B - 1], start[B - 1] = 4, 14, 3, 30
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    _, P32 = calib_P(Hkv)
+    rope, rn, inter = rope_of((128, False))
+    for bad in (False, True):
+        cache = make_cache(B, Hkv, page, m, 3, seed=71)
+        if bad:
+            n200 = 200 + next(i for i in range(100) if n[200 + i] > 0 and start[200 + i] // page == (start[200 + i] + n[200 + i] - 1) // page)
+            cache.block_table[n200, start[n200] // page] = -1
+        k, v = rows_of(rng, sum(n), Hkv, "f32"), rows_of(rng, sum(n), Hkv, "f32")
+        before = snap(cache)
+        aq.aqua_paged_append(cache.desc, tdev(k), tdev(v), torch.tensor(start, dtype=torch.int32, device="cuda"),
+                             tdev(P32), cu_new=torch.from_numpy(cu).cuda(), rope=rope)
+        torch.cuda.synchronize()
+        check_append(cache, before, k, v, P32, start, cu, rn, inter, skip=(n200,) if bad else ())
+        assert aq.aqua_paged_status(cache.desc) == (aq.abi.AQUA_ERR_ARG if bad else aq.AQUA_OK)
