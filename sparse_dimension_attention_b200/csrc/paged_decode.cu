@@ -45,10 +45,11 @@
 //
 // Measured, three launches replayed from a graph: 131072 tokens x 8 heads 56 us
 // (268 MB of rows a head kept: 4.7 TB/s), 32 sequences of up to 32768 tokens, 8
-// heads of 8 queries, 183 to 192 us (4.9 TB/s), 8 x 8192 tokens 37 us.  Bound by
-// the softmax warps' chain of a tile (2200 to 3500 cycles from its scores to its
-// p, two blocks an SM) and, in short jobs, by the 9 us until the selection is
-// done and the first tile is through.
+// heads of 8 queries, 181 to 192 us (4.9 TB/s), 8 x 8192 tokens 37 us.  With up to
+// four heads a group the middle of a job is bound by memory (1.5 us a tile and
+// block, two blocks an SM), with eight by the softmax warps' chain of a tile; to
+// that come 9 us until the selection is done and the first scores are there,
+// and 4 us of tail and merge.
 //
 // edgentiq, "How AQUA Works", Online Inference: scores on the selected
 // dimensions, softmax, weighted sum of the unprojected values.
