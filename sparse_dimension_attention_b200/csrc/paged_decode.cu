@@ -573,7 +573,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     for (int y = 0; y < kThreads / 32; ++y) total += ms.scan[y];
   }
   const Pieces pieces(total * c.Hkv, gridDim.x);
-  if (blockIdx.x >= pieces.nb) return;
+  if (blockIdx.x >= pieces.nb) {
+    // The merge waits for this grid alone: with no tokens at all, where every block leaves here, only this wait
+    // orders it and what comes after it behind the selection (its counts, its zeros in out).
+    pdl_wait();
+    return;
+  }
   {
     const long long t0 = pieces.start(blockIdx.x);
     long long before = 0;
