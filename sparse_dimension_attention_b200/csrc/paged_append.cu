@@ -770,8 +770,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(__uint_as_float(x[e]) + __uint_as_float(y[e])));
-        if (!(m * unit < INFINITY)) {        // an infinity among them: the largest finite one
-          m = 0.f;
+        if (__any_sync(0xffffffffu, !(m * unit < INFINITY))) {   // an infinity in one of the warp's rows: the largest finite ones
+          m = 0.f;                           // (by the whole warp: the loads from tensor memory are its joint business)
 #pragma unroll 1
           for (int e = 0; e < 32; ++e) {
             uint32_t z0, z1;

@@ -42,3 +42,48 @@ def test_decode_of_a_batch_without_tokens(B, Hq, Hkv, od, rejected):
         assert bool((out == 0).all()) and bool((lse == -np.inf).all()) and torch.equal(sel, seen[0][2])
     assert int(seen[0][2].min()) >= 0 and int(seen[0][2].max()) < m
     assert aq.aqua_paged_status(cache.desc) == (aq.abi.AQUA_ERR_ARG if rejected else aq.AQUA_OK)
+
+
+# ------------------------------------------------------------------ append at the ends of the range
+
+F32_MAX = float(np.finfo(np.float32).max)
+
+
+@pytest.mark.parametrize("n,io", [(300, "f32"), (300, "bf16"), (20, "f32")])       # tensor-core tiles, CUDA cores
+def test_append_projections_past_f32(n, io):
+    """Finite rows whose projection leaves f32 in one dimension: the finite ones set the page's scale, the
+    others saturate or keep their own code, rows beside them (of the same warp too) are what they would be."""
+    Hkv, page, m = 8, 64, 96
+    rng = np.random.default_rng(81)
+    _, P32 = calib_P(Hkv)
+    P = P32.astype(np.float64)
+    cache = make_cache(1, Hkv, page, m, -(-n // page), seed=82)
+    k, v = rows_of(rng, n, Hkv, io), rows_of(rng, n, Hkv, io)
+    big = torch.tensor(3e38).to(DT[io]).double().item()
+    huge = [(3, 1, 5, 1.0), (9, 6, 90, -1.0)] + ([(100, 3, 0, 1.0), (107, 3, 64, -1.0), (299, 0, 17, 1.0)] if n > 299 else [])
+    for t, h, j, sign in huge:
+        k[t, h] = big * sign * np.sign(P[h, :, j])
+    kt = np.einsum("nhi,hij->nhj", k, P)[..., :m]
+    err = 132 * 2.0 ** -24 * np.einsum("nhi,hij->nhj", np.abs(k), np.abs(P))[..., :m]
+    # f32 sums within err of the largest number may go either way
+    over, finite = np.abs(kt) - err > F32_MAX, np.abs(kt) + err <= F32_MAX
+    assert over.sum() >= len(huge)
+    aq.aqua_paged_append(cache.desc, tdev(k, DT[io]), tdev(v, DT[io]), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                         tdev(P32), cu_new=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    a = snap(cache)
+    for p0 in range(-(-n // page)):
+        rows, pid = slice(p0 * page, min(n, p0 * page + page)), int(a["block_table"][0, p0])
+        for h in range(Hkv):
+            s = float(a["k_scale"][pid, h])
+            x, e = kt[rows, h], err[rows, h]
+            least = np.where(finite[rows, h], np.abs(x) - e, 0.0).max()
+            most = np.where(over[rows, h], 0.0, np.minimum(np.abs(x) + e, F32_MAX)).max()
+            assert PO.page_scale(max(least, 0.0)) <= s <= PO.page_scale(most)
+            got = PO.e4m3_decode(a["k_pages"][pid, h])[:, :x.shape[0]].T
+            ok = (PO.e4m3_round((x - e) / s) <= got) & (got <= PO.e4m3_round((x + e) / s))
+            # a sum that left f32 was an infinity (448), or never took the form of an f32 number (its own code)
+            ok |= ~finite[rows, h] & (got == np.sign(x) * 448)
+            assert np.all(ok), (p0, h)
+            np.testing.assert_array_equal(PO.e4m3_decode(a["v_pages"][pid, h][:x.shape[0]]),
+                                          PO.e4m3_round(v[rows, h] / float(a["v_scale"][pid, h])))
+    assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
