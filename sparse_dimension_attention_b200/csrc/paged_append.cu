@@ -172,7 +172,7 @@ __device__ __forceinline__ float page_scale(float amax, float old, int fill) {
 // sums input dims 16w .. 16w+15) and their eight partial sums added in order.
 // Bound by the reads of the rows from shared memory, 0.3 us a token and block.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c, AppendParams a, int segs) {
+__global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c, AppendParams a) {
   extern __shared__ __align__(16) float dyn[];
   float* kt = dyn;                                         // [page][D] projected keys
   float* part = kt + ((size_t)D << c.page_log2);           // [kWarps][kGroup][D]
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
 #pragma unroll
   for (int i = 0; i < kRows; ++i) p[i] = __ldg(Pg + (w * kRows + i) * (D / 4) + lane);
 #pragma unroll 1
-  for (int seg = blockIdx.x; seg < segs; seg += gridDim.x) {
+  for (int seg = blockIdx.x;; seg += gridDim.x) {          // to the last segment the device data give
     __syncthreads();                         // the search's shared words are free again
     Segment s;
     if (!find_segment(a, c, seg, s)) return;
@@ -1107,12 +1107,12 @@ int launch_run(const PagedView& c, const AppendParams& a, cudaStream_t st) {
   const int smem = ((D << c.page_log2) + kWarps * kGroup * D + 2 * kGroup * D) * (int)sizeof(float);
   const int rc = set_smem_limit(paged_append_run_kernel<T>, smem, "paged_append_run_kernel");
   if (rc != AQUA_OK) return rc;
-  // a run of n >= 1 tokens touches at most (n - 2) / page + 2 pages, and at most n
+  // a run of n >= 1 tokens touches at most (n - 2) / page + 2 pages, and at most n (of runs that share no rows)
   const long long by_page = a.n_tokens / (1 << c.page_log2) + 2LL * c.B;
   const int segs = (int)(by_page < a.n_tokens ? by_page : a.n_tokens);
   // no more blocks than run at once, two an SM: each reads P once (304 segments of 16 heads: 49 us with a block each)
   const int each = 2 * device_sm_count() / c.Hkv > 0 ? 2 * device_sm_count() / c.Hkv : 1;
-  paged_append_run_kernel<T><<<dim3(segs < each ? segs : each, c.Hkv), kThreads, smem, st>>>(c, a, segs);
+  paged_append_run_kernel<T><<<dim3(segs < each ? segs : each, c.Hkv), kThreads, smem, st>>>(c, a);
   return check_launch("paged_append_run_kernel");
 }
 

@@ -7,7 +7,7 @@ import torch
 import sparse_dimension_attention_b200 as aq
 from oracle import paged_oracle as PO
 from aqua_testlib import calib_P, rel_err_rows, tdev
-from test_gpu_paged import DT, make_cache, rows_of, run_paged_decode, snap
+from test_gpu_paged import DT, check_append, make_cache, rows_of, run_paged_decode, snap
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,20 @@ def test_append_projections_past_f32(n, io):
             np.testing.assert_array_equal(PO.e4m3_decode(a["v_pages"][pid, h][:x.shape[0]]),
                                           PO.e4m3_round(v[rows, h] / float(a["v_scale"][pid, h])))
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+def test_append_runs_that_share_rows():
+    """cu_new that steps back between runs: those entries are reported and left alone, every run that is ascending is
+    appended whole, although together they have more tokens than there are rows."""
+    Hkv, page, m, pairs, n = 2, 16, 32, 13, 64
+    rng = np.random.default_rng(83)
+    _, P32 = calib_P(Hkv)
+    cache = make_cache(2 * pairs - 1, Hkv, page, m, 5, seed=84)
+    k, v = rows_of(rng, n, Hkv, "f32"), rows_of(rng, n, Hkv, "f32")
+    cu = np.array([0, n] * pairs, dtype=np.int32)
+    start = [3] * cache.B
+    before = snap(cache)
+    aq.aqua_paged_append(cache.desc, tdev(k), tdev(v), torch.tensor(start, dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=torch.from_numpy(cu).cuda())
+    check_append(cache, before, k, v, P32, start, cu, None, False, skip=tuple(range(1, cache.B, 2)))
+    assert aq.aqua_paged_status(cache.desc) == aq.abi.AQUA_ERR_ARG
