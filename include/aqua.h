@@ -450,9 +450,12 @@ AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new,
  *              a workspace each.
  * Hq a multiple of Hkv with Hq / Hkv in 1 .. 8.  A sequence of length 0 gets a
  * zero output and lse = -inf.  Scores, softmax statistics and sums are f32.
- * Codes enter the tensor cores as they are, queries and probabilities as sums
- * of e4m3 parts: 15 and 11 bits or more for a bf16 output, about 24 for an f32
- * one.  A query with an infinity or NaN among its kept dimensions gives NaN.
+ * Codes enter the tensor cores as they are.  For an f32 output queries are held
+ * to 2^-24 and weights to 2^-22 of themselves; for a bf16 one queries to 2^-16
+ * (the scores and lse too) and weights to 2^-11, as in f16.  Relative to the
+ * largest weight of a head, one below 2^-26 has fewer bits and one below 2^-37
+ * (f32 output: 2^-49) may be lost.  A query with an infinity or NaN among its kept
+ * dimensions gives NaN.
  */
 AQUA_API size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq);
 AQUA_API int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,

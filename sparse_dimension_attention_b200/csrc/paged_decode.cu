@@ -23,9 +23,15 @@
 // Both products run on tcgen05 (kind::f8f6f4) straight from the codes: a tile's
 // kept key rows [dim][128 tokens] and its value rows [token][128 dims] are each
 // the M-major A operand as they lie in the pages, so no code is ever converted.
-// The B operands are q~ and p as sums of e4m3 parts, 16 times finer each: four
-// parts of q~ and three of p (15 and 11 bits or more) for a bf16 output, six of
-// both (about 24 bits) for an f32 one.
+// The B operands are sums of 8-bit parts.  q~: e4m3, 16 times finer each, four for
+// a bf16 output (15 bits or more), six for an f32 one (about 24).  p: e5m2, whose
+// five exponent bits are those of f16.  For a bf16 output p is rounded once to f16
+// and cut exactly into four parts, 8 times finer each; for an f32 one what that
+// rounding left is a second f16 number of four parts (2^-22).  With 2^12 to 2^15
+// for the largest p, a weight down to 2^-26 of it keeps f16's 11 bits, and one is
+// lost only below 2^-37 (2^-49): a key that outweighs a long tail and has a value
+// of nearly nothing leaves the tail its share.  (Three e4m3 parts, a grid of 2^-23
+// of the largest, lost such a tail from 15 nats on.)
 // N = parts x heads is 16 to 64 columns; a product of 128 x 128 x N reads 16 KB
 // of A, so the columns cost next to nothing.  (Products on mma.sync f16, with
 // every code converted in registers, left the kernel bound by instructions: 73 us
@@ -430,7 +436,7 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem], e4m3 in, f32 accumulate
+// D[tmem] (+)= A[smem] * B[smem], 8-bit floats in, f32 accumulate
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           bool accumulate) {
   asm volatile(
@@ -472,9 +478,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(1024 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// kind::f8f6f4: e4m3 A (M-major) and B (K-major), f32 D, 128 x N
-__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
-  return (1u << 4) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
+// kind::f8f6f4: e4m3 A (M-major), e4m3 or e5m2 B (K-major), f32 D, 128 x N
+enum Fp8Type { kE4m3 = 0, kE5m2 = 1 };
+__host__ __device__ constexpr uint32_t idesc_f8(int N, Fp8Type b) {
+  return (1u << 4) | ((uint32_t)b << 10) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(TT >> 4) << 24);
 }
 
 // Bounded wait that gives up at once when another role did; the first to give up reports.  The value warp and
@@ -535,14 +542,19 @@ __device__ __forceinline__ void next_tile(const PagedView& c, const DecodeP& p, 
 }
 
 constexpr float kLazy = 3.f;        // the reference M is raised when a score exceeds it by 2^3
-constexpr float kPScale = 5.f;      // p is held times 2^5: at most 2^8, below e4m3's 448
+constexpr float kPScale = 12.f;     // p is held times 2^12: at most 2^15, below the largest f16 and e5m2 numbers
+
+// the four columns of p's f16 number, each part 8 times finer than the one before
+__device__ __forceinline__ float join_p(const float* v) {
+  return fmaf(fmaf(fmaf(v[3], 0.125f, v[2]), 0.125f, v[1]), 0.125f, v[0]);
+}
 
 // Columns of the B operands: head h, part i in column STR h + i; NH heads.
 template <int STR, int NH>
 struct Cols {
   static constexpr int N = STR * NH;
   static constexpr int QPARTS = STR == 4 ? 4 : 6;
-  static constexpr int PPARTS = STR == 4 ? 3 : 6;
+  static constexpr int PPARTS = STR;       // four of an f16 number, or of two
   static constexpr int TMEM = N <= 16 ? 64 : (N <= 32 ? 128 : 256);   // S(even), S(odd), O
   static constexpr int CTAS = N <= 32 ? 2 : 1;                        // blocks an SM (shared memory)
   static __host__ __device__ int smem(int m) {
@@ -870,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
   } else if (w == kMmaWarp) {
     // ================= products =================
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(N);
+      constexpr uint32_t idesc = idesc_f8(N, kE4m3), idesc_p = idesc_f8(N, kE5m2);
       uint32_t firsts = 0;                    // bit t & 31: tile t is the first of its part
       int n_all = 0x7fffffff;                 // tiles, once known
       bool ok = true;
@@ -912,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         const bool first = (firsts >> (t & 31)) & 1u;
 #pragma unroll
         for (int k = 0; k < TT / 32; ++k)
-          tc_mma_f8(tmem + 2 * N, ad + k * (32 * D >> 4), bd + k * 2, idesc, k > 0 || !first);
+          tc_mma_f8(tmem + 2 * N, ad + k * (32 * D >> 4), bd + k * 2, idesc_p, k > 0 || !first);
         tc_commit(&ms.pv_done[t & 1]);
         tc_commit(&ms.v_empty[t % kVStages]);
       }
@@ -1019,20 +1031,28 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 #pragma unroll
       for (int h = 0; h < NH; h += 2) {
         if (h >= G) break;
-        float a0 = fast_exp2(x[h] - (ref[h] == -INFINITY ? 0.f : ref[h]) + kPScale);
-        float a1 = h + 1 < G ? fast_exp2(x[h + 1] - (ref[h + 1] == -INFINITY ? 0.f : ref[h + 1]) + kPScale) : 0.f;
+        const float a0 = fast_exp2(x[h] - (ref[h] == -INFINITY ? 0.f : ref[h]) + kPScale);
+        const float a1 = h + 1 < G ? fast_exp2(x[h + 1] - (ref[h + 1] == -INFINITY ? 0.f : ref[h + 1]) + kPScale) : 0.f;
         l[h] = fmaf(a0, iv, l[h]);
         l[h + 1] = fmaf(a1, iv, l[h + 1]);
+        // two heads as a pair of f16 numbers; the upper byte of one is the e5m2 number that its lower bits are cut off
+        // from, what is left times 8 is exact
+        __half2 p2 = __floats2half2_rn(a0, a1);
+        __half2 rest;                          // what the rounding left, 2^12 times (at most half a step of 2^4)
+        if (STR == 8) {
+          const float2 f = __half22float2(p2);
+          rest = __floats2half2_rn((a0 - f.x) * 4096.f, (a1 - f.y) * 4096.f);
+        }
 #pragma unroll
         for (int i = 0; i < CC::PPARTS; ++i) {
-          const uint16_t code = f32x2_to_e4m3x2(a0, a1);
+          if (i == 4) p2 = rest;
+          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&p2);
           const int n0 = h * STR + i, n1 = n0 + STR;
-          pb[n0 * TT + ((pchunk ^ (n0 & 7)) << 4)] = (uint8_t)code;
-          pb[n1 * TT + ((pchunk ^ (n1 & 7)) << 4)] = (uint8_t)(code >> 8);
-          if (i + 1 < CC::PPARTS) {
-            const float2 back = e4m3x2_to_f32x2(code);
-            a0 = (a0 - back.x) * 16.f;
-            a1 = (a1 - back.y) * 16.f;
+          pb[n0 * TT + ((pchunk ^ (n0 & 7)) << 4)] = (uint8_t)(bits >> 8);
+          pb[n1 * TT + ((pchunk ^ (n1 & 7)) << 4)] = (uint8_t)(bits >> 24);
+          if ((i & 3) < 3) {
+            const uint32_t top = bits & 0xff00ff00u;
+            p2 = __hmul2(__hsub2(p2, *reinterpret_cast<const __half2*>(&top)), __float2half2_rn(8.f));
           }
         }
       }
@@ -1069,9 +1089,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         for (int hl = 0; hl < 16 / STR; ++hl) {
           const int h = cb / STR + hl;
           if (h >= G) continue;
-          float O = v[hl * STR + CC::PPARTS - 1];
-#pragma unroll
-          for (int i = CC::PPARTS - 2; i >= 0; --i) O = fmaf(O, 1.f / 16.f, v[hl * STR + i]);
+          float O = join_p(v + hl * STR);
+          if (STR == 8) O = fmaf(join_p(v + hl * STR + 4), 1.f / 4096.f, O);
           const float L = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
           // p was held times 2^kPScale, so M + log2 l is off by it
           const float M = ref[h] - kPScale;

@@ -7,7 +7,7 @@ import torch
 import sparse_dimension_attention_b200 as aq
 from oracle import paged_oracle as PO
 from aqua_testlib import calib_P, rel_err_rows, tdev
-from test_gpu_paged import DT, check_append, make_cache, rows_of, run_paged_decode, snap
+from test_gpu_paged import DT, check_append, make_cache, oracle_decode, rows_of, run_paged_decode, snap
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,92 @@ def test_append_runs_that_share_rows():
                          cu_new=torch.from_numpy(cu).cuda())
     check_append(cache, before, k, v, P32, start, cu, None, False, skip=tuple(range(1, cache.B, 2)))
     assert aq.aqua_paged_status(cache.desc) == aq.abi.AQUA_ERR_ARG
+
+
+# ------------------------------------------------------------------ weights far apart, long sums
+
+def pooled(Hkv, B, table, codes_k, codes_v):
+    """A cache of B alike sequences whose table names pages of a small pool many times."""
+    pool, page = codes_k.shape[0], codes_k.shape[3]
+    one = torch.ones(pool, Hkv, device="cuda")
+    return aq.AquaPagedCache.from_buffers(codes_k.cuda(), codes_v.cuda(), one, one.clone(),
+                                          torch.tensor(np.repeat(table[None], B, 0), dtype=torch.int32, device="cuda"))
+
+
+def pooled_ref(cache, q, n, k):
+    """Output and lse in f64 (P = 1, scale 1 / sqrt(128)); the pages before the last are whole.  Also every token's
+    weight relative to the largest of its head, and how often each occurs."""
+    pool, H, m, page = cache.k_pages.shape
+    G = q.shape[1] // H
+    table = cache.block_table[0].long().cpu().numpy()[:-(-n // page)]
+    count = np.repeat(np.bincount(table, minlength=pool)[:, None], page, 1).astype(np.float64)
+    if n % page:
+        count[table[-1], n % page:] -= 1
+    c = torch.from_numpy(count).cuda().reshape(-1)
+    out, lse, rel = [], [], []
+    for h in range(H):
+        kk = cache.k_pages[:, h].view(torch.float8_e4m3fn).double().permute(1, 0, 2).reshape(m, -1)
+        vv = cache.v_pages[:, h].view(torch.float8_e4m3fn).double().reshape(-1, 128)
+        qt = q[0, h * G:(h + 1) * G].double()
+        keep = qt[:, :m].abs().topk(k, dim=1).indices
+        qm = torch.zeros(G, m, dtype=torch.float64, device="cuda").scatter_(1, keep, qt.gather(1, keep))
+        s = (qm @ kk / 128 ** 0.5).masked_fill(c == 0, -np.inf)
+        top = s.amax(1, keepdim=True)
+        w = torch.exp(s - top)
+        total = (w * c).sum(1, keepdim=True)
+        out.append((w * c) @ vv / total)
+        lse.append((top + total.log())[:, 0])
+        rel.append(w)
+    return torch.cat(out), torch.cat(lse), torch.cat(rel), c
+
+
+def decode_pooled(cache, q, n, k, od):
+    B, Hq = cache.B, q.shape[1]
+    P = torch.eye(128, device="cuda").expand(cache.Hkv, 128, 128).contiguous()
+    out = torch.empty(B, Hq, 128, dtype=DT[od], device="cuda")
+    lse = torch.empty(B, Hq, device="cuda")
+    ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, Hq),), 0xFF, dtype=torch.uint8, device="cuda")
+    aq.aqua_paged_decode_attn(cache.desc, q.repeat(B, 1, 1), torch.tensor([n] * B, dtype=torch.int32, device="cuda"), P, Hq,
+                              k, out, ws, lse_out=lse)
+    assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+    return out.double(), lse.double()
+
+
+@pytest.mark.parametrize("B,G,n,at,od", [
+    (1, 8, 131072, 0, "bf16"), (1, 4, 131072, 700, "bf16"), (1, 8, 131072, 1023, "bf16"), (1, 8, 100, 0, "bf16"),
+    (1, 1, 1280, 3, "bf16"), (300, 8, 32768, 0, "bf16"), (300, 4, 32768, 5, "bf16"), (300, 8, 32768, 250, "bf16"),
+    (1, 8, 131072, 0, "f32"), (1, 4, 131072, 700, "f32"), (1, 8, 131072, 1023, "f32"), (1, 8, 100, 0, "f32"),
+    (1, 1, 1280, 3, "f32"),
+])
+def test_decode_one_dominant_key_over_a_long_tail(B, G, n, at, od):
+    """One key 12 to 20 nats above all others with a value of nearly nothing: the output is what the others add up to.
+
+    What the weights lose: rounded to f16 they are off by half a step at most, 2^-11 of themselves or 2^-25 where the
+    largest is 2^12 or more, so 2^-37 of that; for an f32 output the rest is rounded to f16 again, 2^-22 and 2^-49.
+    Over a sum of weights the second is n steps against their sum.  Then q~ (off by 2^-16 and 2^-24, which moves scores
+    of up to 20 by 20 times that), the output's own rounding (eps / 2 of bf16, 2^-8) and 1e-5 for all sums in f32."""
+    page, m, k, pool = 128, 32, 16, 33
+    g = torch.Generator().manual_seed(90)
+    ck = torch.randint(0x10, 0x28, (pool, 1, m, page), generator=g) + 128 * torch.randint(0, 2, (pool, 1, m, page), generator=g)
+    cv = torch.randint(0x30, 0x38, (pool, 1, page, 128), generator=g)
+    ck[:, 0, 0] = 0
+    ck[0, 0, :, 37] = 0
+    ck[0, 0, 0, 37] = 0x58                     # 16
+    cv[0, 0, 37, :64], cv[0, 0, 37, 64:] = 0, 1
+    table = np.random.default_rng(91).integers(1, pool, -(-n // page))
+    table[at] = 0
+    cache = pooled(1, B, table, ck.to(torch.uint8), cv.to(torch.uint8))
+    gaps = [17.0] if G == 1 else list(np.linspace(12, 20, G))
+    q = torch.zeros(1, G, 128)
+    q[0, :, 1:k] = 0.5 + torch.rand(G, k - 1, generator=g)
+    q[0, :, 0] = torch.tensor(gaps) / 16 * 128 ** 0.5
+    q = q.cuda()
+    got, lse = decode_pooled(cache, q, n, k, od)
+    ref, lref, w, c = pooled_ref(cache, q, n, k)
+    tail = (c.sum() - 1) / ((w * c).sum(1) - 1)          # tokens over the sum of their weights (the dominant one's is 1)
+    half_step, grid, query, own = (2.0 ** -11, 2.0 ** -37, 2.0 ** -16, 2.0 ** -8) if od == "bf16" else (2.0 ** -22, 2.0 ** -49, 2.0 ** -24, 0)
+    tol = half_step + tail * grid + 20 * query + own + 1e-5
+    for half in (slice(0, 64), slice(64, 128)):
+        err = ((got - ref)[..., half].norm(dim=-1) / ref[:, half].norm(dim=-1)).amax(0)
+        assert bool((err <= tol).all()), (err.tolist(), tol.tolist())
+    assert float((lse - lref).abs().max()) <= (20 * 2.0 ** -16 if od == "bf16" else 20 * 2.0 ** -22)
