@@ -384,7 +384,8 @@ struct TileInfo {
   int q;                   // buffer with the unit's queries
   int flags;
 };
-enum TileFlag { kFirst = 1, kLast = 2, kEnd = 4 };   // of the piece's part of a unit; of the block's work
+enum TileFlag { kFirst = 1, kLast = 2, kEnd = 4,     // of the piece's part of a unit; of the block's work
+                kFresh = 8 };                        // O starts from zero
 
 struct AttendMisc {
   uint64_t known[kVStages];                 // a tile's info is written
@@ -543,6 +544,12 @@ __device__ __forceinline__ void next_tile(const PagedView& c, const DecodeP& p, 
 
 constexpr float kLazy = 3.f;        // the reference M is raised when a score exceeds it by 2^3
 constexpr float kPScale = 12.f;     // p is held times 2^12: at most 2^15, below the largest f16 and e5m2 numbers
+
+// The tensor cores cut each sum they extend off, always towards zero: over the thousands of extensions that a long
+// unit has in one block the losses add up (2e-4 of the output after 3000 tiles).  For f32 outputs O goes to registers
+// every kFlush tiles, 64 extensions: at most 64 / 2 steps of 2^-23, 4e-6.  l does the same in each thread, so that
+// small weights are added to each other before they meet a large one (1.2e-5 off after 256 tiles otherwise).  A bf16 output's rounding covers 2^-10, four thousand tiles of a unit in a block.
+constexpr int kFlush = 16;
 
 // the four columns of p's f16 number, each part 8 times finer than the one before
 __device__ __forceinline__ float join_p(const float* v) {
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         // a part that does not start the piece is its second
         ti.slot = unit_end && seg_first == 0 ? -1 : 2 * piece + (begin + (cur.tile - seg_first) < stop_at - left ? 1 : 0);
         ti.q = ord & 1;
-        ti.flags = (change ? kFirst : 0) | (unit_end || left == 1 ? kLast : 0) | (end ? kEnd : 0);
+        ti.flags = (change ? kFirst : 0) | (change || (STR == 8 && (cur.tile - seg_first) % kFlush == 0) ? kFresh : 0) | (unit_end || left == 1 ? kLast : 0) | (end ? kEnd : 0);
         ms.info[st] = ti;
         mbar_arrive(&ms.known[st]);
       }
@@ -883,12 +890,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     // ================= products =================
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_f8(N, kE4m3), idesc_p = idesc_f8(N, kE5m2);
-      uint32_t firsts = 0;                    // bit t & 31: tile t is the first of its part
+      uint32_t fresh = 0;                     // bit t & 31: O starts from zero with tile t
       int n_all = 0x7fffffff;                 // tiles, once known
       bool ok = true;
       auto issue_s = [&](int t) {
         const int fl = ms.info[t % kVStages].flags;
-        firsts = (firsts & ~(1u << (t & 31))) | ((fl & kFirst ? 1u : 0u) << (t & 31));
+        fresh = (fresh & ~(1u << (t & 31))) | ((fl & kFresh ? 1u : 0u) << (t & 31));
         if (fl & kEnd) n_all = t + 1;
         fence_proxy_async_smem();
         tc_fence_after();
@@ -921,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         tc_fence_after();
         const uint64_t ad = smem_desc(smem0 + (t % kVStages) * kStageV);
         const uint64_t bd = smem_desc(smem0 + off_p + (t & 1) * N * TT);
-        const bool first = (firsts >> (t & 31)) & 1u;
+        const bool first = (fresh >> (t & 31)) & 1u;
 #pragma unroll
         for (int k = 0; k < TT / 32; ++k)
           tc_mma_f8(tmem + 2 * N, ad + k * (32 * D >> 4), bd + k * 2, idesc_p, k > 0 || !first);
@@ -945,6 +952,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
     const uint32_t pcol = (uint32_t)(tid & 15);
     const uint32_t pchunk = (uint32_t)(tid >> 4);
     bool begun = false;                       // O holds tiles of this part
+    float acc[STR == 8 ? NH : 1], lacc[STR == 8 ? NH : 1];      // what it held before it started afresh, and l likewise
+    // O of head h of the sixteen columns v, from column cb on
+    auto head_of = [&](const float* v, int hl) {
+      const float O = join_p(v + hl * STR);
+      return STR == 8 ? fmaf(join_p(v + hl * STR + 4), 1.f / 4096.f, O) : O;
+    };
     for (int t = 0;; ++t) {
       const int st = t % kVStages, buf = t & 1;
       wait(&ms.known[st], (t / kVStages) & 1);
@@ -955,7 +968,25 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         for (int h = 0; h < NH; ++h) {
           ref[h] = -INFINITY;
           l[h] = 0.f;
+          if (STR == 8) acc[h] = lacc[h] = 0.f;
         }
+      } else if (STR == 8 && (ti.flags & kFresh)) {
+        wait(&ms.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int cb = 0; cb < N; cb += 16) {
+          float v[16];
+          tmem_ld16(lane_base + 2 * N + cb, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hl = 0; hl < 16 / STR; ++hl) acc[cb / STR + hl] += head_of(v, hl);
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          lacc[h] += l[h];
+          l[h] = 0.f;
+        }
+        begun = false;
       }
       wait(&ms.s_full[buf], (t >> 1) & 1);    // and the scales have landed, before the scores were issued
       tc_fence_after();
@@ -1006,6 +1037,10 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
             al[h] = fast_exp2(ref[h] - m);
             ref[h] = m;
             l[h] *= al[h];
+            if (STR == 8) {
+              acc[h] *= al[h];
+              lacc[h] *= al[h];
+            }
           }
         }
         if (begun) {
@@ -1073,6 +1108,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
         if (h >= G) break;
+        if (STR == 8) l[h] += lacc[h];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
         if (lane == 0) ms.red[w][h] = l[h];
@@ -1089,8 +1125,8 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         for (int hl = 0; hl < 16 / STR; ++hl) {
           const int h = cb / STR + hl;
           if (h >= G) continue;
-          float O = join_p(v + hl * STR);
-          if (STR == 8) O = fmaf(join_p(v + hl * STR + 4), 1.f / 4096.f, O);
+          float O = head_of(v, hl);
+          if (STR == 8) O += acc[h];
           const float L = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
           // p was held times 2^kPScale, so M + log2 l is off by it
           const float M = ref[h] - kPScale;

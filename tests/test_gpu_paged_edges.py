@@ -160,6 +160,7 @@ def decode_pooled(cache, q, n, k, od):
     (1, 1, 1280, 3, "bf16"), (300, 8, 32768, 0, "bf16"), (300, 4, 32768, 5, "bf16"), (300, 8, 32768, 250, "bf16"),
     (1, 8, 131072, 0, "f32"), (1, 4, 131072, 700, "f32"), (1, 8, 131072, 1023, "f32"), (1, 8, 100, 0, "f32"),
     (1, 1, 1280, 3, "f32"),
+    (300, 8, 32768, 0, "f32"), (300, 4, 32768, 5, "f32"), (300, 8, 32768, 250, "f32"),
 ])
 def test_decode_one_dominant_key_over_a_long_tail(B, G, n, at, od):
     """One key 12 to 20 nats above all others with a value of nearly nothing: the output is what the others add up to.
@@ -193,3 +194,23 @@ def test_decode_one_dominant_key_over_a_long_tail(B, G, n, at, od):
         err = ((got - ref)[..., half].norm(dim=-1) / ref[:, half].norm(dim=-1)).amax(0)
         assert bool((err <= tol).all()), (err.tolist(), tol.tolist())
     assert float((lse - lref).abs().max()) <= (20 * 2.0 ** -16 if od == "bf16" else 20 * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("G,tokens,od,spread", [(4, 30_000_000, "f32", 0), (8, 100_000_000, "f32", 0), (8, 30_000_000, "f32", 1),
+                                                (1, 3_000_000, "f32", 1), (4, 100_000_000, "bf16", 1)])
+def test_decode_long_sums_of_one_sign(G, tokens, od, spread):
+    """Values of one sign over hundreds of tiles a block: sums that are cut off would all lose.
+    f32 outputs 1e-5 as everywhere; bf16: its own rounding (eps / 2, 2^-8) and what the header allows the sums, 2^-10."""
+    page, m, k, pool = 128, 16, 8, 64
+    g = torch.Generator().manual_seed(92)
+    ck = torch.randint(0x28, 0x40, (pool, 1, m, page), generator=g) if spread else torch.randint(0x10, 0x28, (pool, 1, m, page), generator=g)
+    ck = ck + 128 * torch.randint(0, 2, (pool, 1, m, page), generator=g)
+    cv = torch.randint(0x30, 0x38, (pool, 1, page, 128), generator=g)
+    n = tokens // page * page
+    cache = pooled(1, 1, np.random.default_rng(93).integers(0, pool, n // page), ck.to(torch.uint8), cv.to(torch.uint8))
+    q = (torch.randn(1, G, 128, generator=g) * (4 if spread else 1)).cuda()
+    got, lse = decode_pooled(cache, q, n, k, od)
+    ref, lref, _, _ = pooled_ref(cache, q, n, k)
+    err = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).amax(0)
+    assert float(err.max()) <= (1e-5 if od == "f32" else 2.0 ** -8 + 2.0 ** -10), err.tolist()
+    assert float((lse - lref).abs().max()) <= (1e-5 if od == "f32" else 2e-4)
