@@ -456,8 +456,10 @@ AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new,
  * to 2^-24 and weights to 2^-22 of themselves; for a bf16 one queries to 2^-16
  * (the scores and lse too) and weights to 2^-11, as in f16.  Relative to the
  * largest weight of a head, one below 2^-26 has fewer bits and one below 2^-37
- * (f32 output: 2^-49) may be lost.  A query with an infinity or NaN among its kept
- * dimensions gives NaN.
+ * (f32 output: 2^-49) may be lost.  A query with an infinity or NaN among its
+ * kept dimensions gives NaN.  A NaN code in a key gives NaN to the heads that
+ * kept its dimension and does nothing to the others (such heads are formed again
+ * by a slow path).
  */
 AQUA_API size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq);
 AQUA_API int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,

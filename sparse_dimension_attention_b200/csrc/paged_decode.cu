@@ -96,11 +96,12 @@ struct DecodeP {
   uint8_t* qpart;        // [n_units][N][D] e4m3 parts of the masked queries: row h * stride + part
   float* qfac;           // [n_units][kMaxG] factor of a head's scores (log2 domain, without the key scale)
   int32_t* prefix;       // [B + 1] tiles of one KV head before each sequence
-  int32_t* ctl;          // [0] pieces taken beyond the first ones, [1] units to merge
+  int32_t* ctl;          // [0] pieces taken beyond the first ones, [1] units to merge, [2] heads to form again
   float2* part_ml;       // [2 * pieces][G] (M, l) of a partial result
   float* part_o;         // [2 * pieces][G][D]
   int4* split;           // [pieces] units to merge, in any order: unit .x has its tiles in pieces .y ... .z; .w: slot of
                          // piece .y's part
+  int32_t* again;        // [n_units * kMaxG] heads with a NaN that is not their query's: unit * kMaxG + head
 };
 
 __device__ __forceinline__ int n_tiles(int len) { return (len + TT - 1) / TT; }
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
   for (int i = tid; i < kMaxG * (D + 8); i += kSelThreads) qd[0][i] = 0.0;
   pdl_wait();
   pdl_launch_dependents();
-  if (tid == 0 && blockIdx.x == 0 && g == 0) p.ctl[0] = p.ctl[1] = 0;
+  if (tid == 0 && blockIdx.x == 0 && g == 0) p.ctl[0] = p.ctl[1] = p.ctl[2] = 0;
   const int b_end = min(c.B, ((int)blockIdx.x + 1) * group);
   int len = 0;
   T x[kEach];                               // as it lies in memory: a conversion here would wait for the load
@@ -274,21 +275,31 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
       // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
       const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
       const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-      if (lane == 0) p.qfac[(size_t)u * kMaxG + w] = __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
       // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
       // most half a step, so 16 times it stays in range)
       uint8_t* dst = p.qpart + ((size_t)u * NH + w) * stride * D + lane;
+      bool lost = false;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         qt[y] *= mul;
-        if (!(fabsf(qt[y]) < INFINITY)) qt[y] = NAN;   // an infinite query makes its scores NaN, not the largest code
+        if (!(fabsf(qt[y]) < INFINITY)) {              // an infinite query makes its scores NaN, not the largest code
+          qt[y] = NAN;
+          lost = true;
+        }
       }
+      lost = __any_sync(0xffffffffu, lost);
+      if (lane == 0)
+        p.qfac[(size_t)u * kMaxG + w] = lost ? NAN : __uint_as_float((uint32_t)(127 - 7 + e) << 23) * p.scale * kLog2e;
 #pragma unroll 1
       for (int i = 0; i < stride; ++i, dst += D) {
         const uint32_t code = i < parts ? f32x4_to_e4m3x4(qt[0], qt[1], qt[2], qt[3]) : 0u;
         const float2 b0 = e4m3x2_to_f32x2((uint16_t)code), b1 = e4m3x2_to_f32x2((uint16_t)(code >> 16));
 #pragma unroll
-        for (int y = 0; y < 4; ++y) dst[32 * y] = (uint8_t)(code >> (8 * y));
+        for (int y = 0; y < 4; ++y) {
+          const uint8_t byte = (uint8_t)(code >> (8 * y));
+          // the first part of a kept entry is never +0, which marks those that are left out
+          dst[32 * y] = i == 0 && byte == 0 && ((word[y] >> lane) & 1u) ? 0x80 : byte;
+        }
         qt[0] = (qt[0] - b0.x) * 16.f;
         qt[1] = (qt[1] - b0.y) * 16.f;
         qt[2] = (qt[2] - b1.x) * 16.f;
@@ -1139,6 +1150,10 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           }
         }
       }
+      if (ti.slot < 0 && tid < G) {           // for the merge kernel: heads with a NaN that their query does not bring
+        const float L = (ms.red[0][tid] + ms.red[1][tid]) + (ms.red[2][tid] + ms.red[3][tid]);
+        if (L != L && p.qfac[(size_t)ti.u * kMaxG + tid] < INFINITY) p.again[atomicAdd(p.ctl + 2, 1)] = ti.u * kMaxG + tid;
+      }
       tc_fence_before();
       named_bar_sync(1, kSoftThreads);        // ms.red is free again
       if (ti.flags & kEnd) break;
@@ -1164,13 +1179,89 @@ constexpr int kMergeFew = 8;
 constexpr int kMaxPieces = 2048;
 constexpr int kPiecesPerBlock = 2;         // a first piece and a later one
 
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView c, DecodeP p, int G) {
+// A NaN code in a dimension that a head left out makes its score on the tensor cores NaN (the query's factor there is
+// 0, and the rows come with every dimension that a head of the group kept).  So a head with a NaN that its query does
+// not bring is formed again here, by one warp over the dimensions it kept: a token a lane for the scores, four dims of
+// the output a lane for the values.  A NaN in a kept dimension shows again and ends the work.  Rare, and slow: 32
+// tokens a time.
+__device__ __noinline__ void form_again(const PagedView& c, const DecodeP& p, int G, int u, int hh, int cols, int stride, int parts) {
+  const int lane = threadIdx.x & 31, b = u / c.Hkv, g = u % c.Hkv;
+  const size_t row = (size_t)b * p.Hq + (size_t)g * G + hh;
+  const float fac = p.qfac[(size_t)u * kMaxG + hh];
+  const uint8_t* q = p.qpart + ((size_t)u * cols + hh * stride) * D + lane;
+  float x[4];                                // dims lane + 32 y
+  uint32_t kept[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    x[y] = 0.f;
+    for (int i = parts - 1; i >= 0; --i) x[y] = fmaf(x[y], 1.f / 16.f, e4m3x2_to_f32x2(q[i * D + 32 * y]).x);
+    kept[y] = __ballot_sync(0xffffffffu, q[32 * y] != 0);
+  }
+  const int n = seq_tokens(c, p, b), mask = (1 << c.page_log2) - 1;
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int t0 = 0; t0 < n; t0 += 32) {
+    const int t = t0 + lane;
+    int pid = -1;
+    if (t < n) pid = __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2));
+    const bool seen = pid >= 0 && pid < c.n_pages;
+    const size_t si = seen ? (size_t)pid * c.Hkv + g : 0;
+    const uint8_t* key = c.k + (seen ? c.kblock(pid, g) + (t & mask) : 0);
+    float s = 0.f;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+#pragma unroll 1
+      for (uint32_t left = kept[y]; left != 0; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        const float xi = __shfl_sync(0xffffffffu, x[y], i);
+        if (seen) s = fmaf(xi, e4m3x2_to_f32x2(key[(size_t)(i + 32 * y) << c.page_log2]).x, s);
+      }
+    }
+    s = seen ? s * (fac * c.ks[si]) : -INFINITY;
+    if (__any_sync(0xffffffffu, s != s)) {
+      M = l = NAN;
+      acc = make_float4(NAN, NAN, NAN, NAN);
+      break;
+    }
+    float top = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, M);
+    const float ref = top == -INFINITY ? 0.f : top, al = fast_exp2(M - ref), e = fast_exp2(s - ref);
+    M = top;
+    l = fmaf(l, al, e);
+    acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
+    const float w = seen ? e * c.vs[si] : 0.f;
+#pragma unroll 1
+    for (uint32_t left = __ballot_sync(0xffffffffu, seen); left != 0; left &= left - 1) {
+      const int i = __ffs(left) - 1, pi = __shfl_sync(0xffffffffu, pid, i);
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const uint32_t v = reinterpret_cast<const uint32_t*>(c.v + c.vblock(pi, g) + (size_t)((t0 + i) & mask) * D)[lane];
+      const float2 v0 = e4m3x2_to_f32x2((uint16_t)v), v1 = e4m3x2_to_f32x2((uint16_t)(v >> 16));
+      acc.x = fmaf(wi, v0.x, acc.x); acc.y = fmaf(wi, v0.y, acc.y);
+      acc.z = fmaf(wi, v1.x, acc.z); acc.w = fmaf(wi, v1.y, acc.w);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const size_t at = row * D + 4 * lane;
+  store_out_elem(p, at, normalised(acc.x, l));
+  store_out_elem(p, at + 1, normalised(acc.y, l));
+  store_out_elem(p, at + 2, normalised(acc.z, l));
+  store_out_elem(p, at + 3, normalised(acc.w, l));
+  if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(M, l);
+}
+
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedView c, const __grid_constant__ DecodeP p, int G, int cols, int stride, int parts) {
   __shared__ __align__(16) float sum[kMergeWarps][D];
   __shared__ float2 ml[kMergeWarps];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   pdl_wait();
   int4 sp = p.split[blockIdx.x / G];       // along with their number: the list has room for more than the blocks
-  const int n_jobs = p.ctl[1] * G;
+  const int n_jobs = p.ctl[1] * G, n_again = p.ctl[2];
+  // whether a sum of weights is NaN and the query is not
+  auto odd = [&](float L, int u, int hh) { return L != L && p.qfac[(size_t)u * kMaxG + hh] < INFINITY; };
   // units cut in eight parts or fewer: a warp each
 #pragma unroll 1
   for (int job = blockIdx.x * kMergeWarps + w; job < n_jobs; job += gridDim.x * kMergeWarps) {
@@ -1202,6 +1293,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView
       L = fmaf(m[i].y, f, L);
       acc.x = fmaf(v[i].x, f, acc.x); acc.y = fmaf(v[i].y, f, acc.y);
       acc.z = fmaf(v[i].z, f, acc.z); acc.w = fmaf(v[i].w, f, acc.w);
+    }
+    if (odd(L, s1.x, hh)) {
+      form_again(c, p, G, s1.x, hh, cols, stride, parts);
+      continue;
     }
     const size_t row = (size_t)(s1.x / c.Hkv) * p.Hq + (size_t)(s1.x % c.Hkv) * G + hh;
     const size_t at = row * D + 4 * lane;
@@ -1253,7 +1348,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView
     *reinterpret_cast<float4*>(&sum[w][4 * lane]) = acc;
     if (lane == 0) ml[w] = make_float2(M, L);
     __syncthreads();
-    if (tid < D) {
+    float all = 0.f;                         // NaN as the whole sum is
+#pragma unroll
+    for (int z = 0; z < kMergeWarps; ++z) all += ml[z].y;
+    if (odd(all, sp.x, hh)) {
+      if (w == 0) form_again(c, p, G, sp.x, hh, cols, stride, parts);
+    } else if (tid < D) {
       float top = -INFINITY;
 #pragma unroll
       for (int z = 0; z < kMergeWarps; ++z) top = fmaxf(top, ml[z].x);
@@ -1271,11 +1371,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedView
     }
     __syncthreads();
   }
+#pragma unroll 1
+  for (int job = blockIdx.x * kMergeWarps + w; job < n_again; job += gridDim.x * kMergeWarps)
+    form_again(c, p, G, p.again[job] / kMaxG, p.again[job] % kMaxG, cols, stride, parts);
 }
 
 // ---------------------------------------------------------------- host side
 struct Layout {
-  size_t umask, qpart, qfac, prefix, ctl, part_ml, part_o, split, total;
+  size_t umask, qpart, qfac, prefix, ctl, part_ml, part_o, split, again, total;
 };
 
 // The workspace does not depend on the output type: room for the widest operands.
@@ -1293,10 +1396,11 @@ Layout layout_of(int B, int Hkv, int G, int blocks) {
   y.qpart = take((size_t)n_units * cols * D);
   y.qfac = take((size_t)n_units * kMaxG * 4);
   y.prefix = take((size_t)(B + 1) * 4);
-  y.ctl = take(2 * 4);
+  y.ctl = take(3 * 4);
   y.part_ml = take((size_t)2 * pieces * G * sizeof(float2));
   y.part_o = take((size_t)2 * pieces * G * D * 4);
   y.split = take((size_t)pieces * sizeof(int4));
+  y.again = take((size_t)n_units * kMaxG * 4);
   y.total = at;
   return y;
 }
@@ -1342,7 +1446,7 @@ int launch_step(const PagedView& c, const DecodeP& p, int G, bool bf16, cudaStre
   if ((rc = check_launch("paged_attend_kernel")) != AQUA_OK) return rc;
   rc = set_largest_carveout(reinterpret_cast<const void*>(paged_merge_kernel), "paged_merge_kernel");
   if (rc != AQUA_OK) return rc;
-  e = launch_pdl(paged_merge_kernel, dim3(blocks), dim3(kMergeWarps * 32), 0, st, c, p, G);
+  e = launch_pdl(paged_merge_kernel, dim3(blocks), dim3(kMergeWarps * 32), 0, st, c, p, G, CC::N, STR, CC::QPARTS);
   if (e != cudaSuccess) return set_error(AQUA_ERR_CUDA, "paged_merge_kernel: %s", cudaGetErrorString(e));
   return check_launch("paged_merge_kernel");
 }
@@ -1369,6 +1473,7 @@ int launch_paged_decode(const PagedView& c, const int32_t* len, const void* q, b
   p.part_ml = reinterpret_cast<float2*>(base + y.part_ml);
   p.part_o = reinterpret_cast<float*>(base + y.part_o);
   p.split = reinterpret_cast<int4*>(base + y.split);
+  p.again = reinterpret_cast<int32_t*>(base + y.again);
   if (out_bf16) return G > 4 ? launch_step<4, 8>(c, p, G, bf16, st) : launch_step<4, 4>(c, p, G, bf16, st);
   return G > 4 ? launch_step<8, 8>(c, p, G, bf16, st) : launch_step<8, 4>(c, p, G, bf16, st);
 }

@@ -214,3 +214,37 @@ def test_decode_long_sums_of_one_sign(G, tokens, od, spread):
     err = ((got - ref).norm(dim=-1) / ref.norm(dim=-1)).amax(0)
     assert float(err.max()) <= (1e-5 if od == "f32" else 2.0 ** -8 + 2.0 ** -10), err.tolist()
     assert float((lse - lref).abs().max()) <= (1e-5 if od == "f32" else 2e-4)
+
+
+# ------------------------------------------------------------------ NaN, and queries at the ends of their range
+
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+def test_decode_nan_keys_in_dimensions_that_a_head_left_out(od):
+    """A head sums over its own dimensions alone: a NaN code in one it did not keep does nothing, wherever the token
+    lies and whether or not another head of the group kept that dimension; in a kept one it makes the head NaN, a
+    query entry of 0 too."""
+    B, Hq, Hkv, page, m, k = 2, 8, 2, 64, 100, 6
+    lens = [1400, 1397]
+    rng = np.random.default_rng(94)
+    cache = make_cache(B, Hkv, page, m, 22, seed=95)
+    for b, h, t, dims in ((0, 0, 3, (7, 50)), (0, 0, 130, (7,)), (0, 0, 300, (50, 20)), (0, 0, 1399, (7, 99)),
+                          (1, 1, 700, (7,)), (1, 1, 1301, (20,)), (0, 1, 901, (3,))):
+        for j in dims:
+            cache.k_pages[int(cache.block_table[b, t // page]), h, j, t % page] = 0x7F if t % 2 else 0xFF
+    q = np.zeros((B, Hq, 128))
+    q[:, :, 30:36] = rng.normal(size=(B, Hq, 6)) + 4.0          # heads 0, 4: dims 30 .. 35
+    for h, j in ((1, 7), (2, 20), (5, 7), (6, 20)):             # and one NaN dimension of sequence 0 or 1
+        q[:, h, j] = 9.0
+    q[:, 3, 30:] = 0.0                                          # heads 3, 7 keep dims 0 .. 5 at 0
+    q[:, 7, 30:] = 0.0
+    P32 = np.broadcast_to(np.eye(128, dtype=np.float32), (Hkv, 128, 128)).copy()
+    got = run_paged_decode(cache, q, lens, tdev(P32), k, None, DT[od], torch.float32)
+    ref = oracle_decode(snap(cache), lens, q, P32, k, None, False, od)
+    np.testing.assert_array_equal(got["sel"], ref["sel"])
+    want = np.zeros((B, Hq), dtype=bool)
+    want[0, 1] = want[0, 2] = want[1, 5] = want[1, 6] = want[0, 7] = True
+    np.testing.assert_array_equal(np.isnan(ref["out"]).any(-1), want)
+    np.testing.assert_array_equal(np.isnan(got["out"]), np.broadcast_to(want[..., None], got["out"].shape))
+    np.testing.assert_array_equal(np.isnan(got["lse"]), want)
+    assert np.max(rel_err_rows(got["out"][~want], ref["out"][~want])) <= (2e-3 if od == "bf16" else 1e-5)
+    assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
