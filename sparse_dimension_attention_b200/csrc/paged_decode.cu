@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
         if (lane == 0) kept[w][y] = word[y];
       }
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-      // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      // 2^(7-e) with mx = f 2^e brings the largest entry to [128, 256): e4m3 reaches 448 and 2^-9.  Any finite entry
+      // has e <= 127; from below 2^-116 on entries get smaller than that, but keep the factor a normal number.
+      const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -116);
       const float mul = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
       // parts: x = x0 + x1 / 16 + x2 / 256 + ..., each the e4m3 number nearest to what is left (a remainder is at
       // most half a step, so 16 times it stays in range)

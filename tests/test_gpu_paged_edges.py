@@ -248,3 +248,19 @@ def test_decode_nan_keys_in_dimensions_that_a_head_left_out(od):
     np.testing.assert_array_equal(np.isnan(got["lse"]), want)
     assert np.max(rel_err_rows(got["out"][~want], ref["out"][~want])) <= (2e-3 if od == "bf16" else 1e-5)
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+@pytest.mark.parametrize("exponent", [100, 118, 126, -100, -118])
+def test_decode_queries_at_the_ends_of_the_range(exponent):
+    """Queries of 2^exponent against keys whose page scales bring the scores back to the usual size."""
+    B, Hq, Hkv, page, m, k, lens = 1, 4, 1, 16, 64, 40, [300]
+    rng = np.random.default_rng(96)
+    cache = make_cache(B, Hkv, page, m, 19, seed=97)
+    cache.k_scale.fill_(2.0 ** (-6 - exponent))
+    q = rng.uniform(0.25, 1.9, size=(B, Hq, 128)) * np.where(rng.random((B, Hq, 128)) < 0.5, -1, 1)
+    q = (q * 2.0 ** exponent).astype(np.float32).astype(np.float64)
+    P32 = np.eye(128, dtype=np.float32)[None]
+    got = run_paged_decode(cache, q, lens, tdev(P32), k, None, torch.float32, torch.float32)
+    ref = oracle_decode(snap(cache), lens, q, P32, k, None, False, "f32")
+    np.testing.assert_array_equal(got["sel"], ref["sel"])
+    assert np.max(rel_err_rows(got["out"], ref["out"])) <= 1e-5
