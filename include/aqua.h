@@ -359,11 +359,6 @@ AQUA_API int aqua_selftest_wait_timeout(aqua_cache* cache, unsigned long long li
  * A page that aqua_paged_append writes must appear once in the table and in one
  * sequence only; full pages that are only read may be shared (prefixes).
  *
- * aqua_paged_append and aqua_paged_decode_attn read P before they wait for the
- * preceding kernel on the stream (everything else only after it), which is safe
- * unless the kernel that wrote P released its dependents early through
- * programmatic dependent launch (no kernel here that writes it does).
- *
  * Device data that the host cannot check is checked by the kernels, which then
  * record AQUA_ERR_ARG in the status word and touch nothing out of bounds: a
  * sequence whose length is negative or beyond max_pages * page_size (or beyond

@@ -518,7 +518,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = ms.tmem;
-  // ---- P of the head, normalised and split (before the wait: the kernel before does not write it)
+  prefetch_head(a.P + (size_t)h * D * D, tid, kTileThreads);
+  pdl_wait();
+  // ---- P of the head, normalised and split
   float p_undo;
   {
     constexpr int kEach = (D * D / 8 + kTileThreads - 1) / kTileThreads;
@@ -557,7 +559,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
     fence_proxy_async_smem();
   }
 
-  pdl_wait();
   // ---- this block's share of the tiles: exclusive sums of the runs' tiles, a pass per kTileThreads sequences
   int n_tiles = 0, i0 = 0, n_my = 0;
   Walk at = {0, 0, 0, 0, 0};
@@ -975,7 +976,7 @@ int launch_tiles(const PagedView& c, const AppendParams& a, cudaStream_t st) {
 
 // One new token for each sequence: a block takes up to kStepGroup sequences of one
 // KV head.  Bound by latency: P (64 KB, from L2) is read once per block into
-// registers before the wait on the previous kernel, and kept there as f64, whose
+// registers and kept there as f64, whose
 // 64 multiply-adds a cycle and SM are enough here; the sums are then exact to f32
 // rounding, so that a code differs from the exact one only on a tie.  Warp t
 // writes token t.  One sequence 4.1 us, 256 of 8 heads 10.3 us, launches replayed
@@ -992,13 +993,14 @@ __global__ void __launch_bounds__(kStepThreads) paged_append_step_kernel(PagedVi
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
   const int col = tid & (D - 1), sl = tid >> 7;
   constexpr int R = D / kStepSlices;
+  prefetch_head(a.P + (size_t)h * D * D, tid, kStepThreads);
+  pdl_wait();
   float pf[R];
   {
     const float* Pg = a.P + ((size_t)h * D + sl * R) * D + col;
 #pragma unroll
     for (int i = 0; i < R; ++i) pf[i] = __ldg(Pg + (size_t)i * D);
   }
-  pdl_wait();
   const int b = blockIdx.x * group + w, nt = min(group, c.B - (int)blockIdx.x * group);
   int pid = -1, slot = 0;
   float v[4] = {0.f, 0.f, 0.f, 0.f};

@@ -128,7 +128,7 @@ __device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -I
 
 // The projection runs on the f64 matrix instruction, heads as rows (those past G are zeros), eight columns of P a
 // warp: on f64 FMAs, every thread a column and all heads, the reads of q~ from shared memory took 5 of 7 us a
-// sequence.  What is left is a chain of latencies: P is loaded before the wait on the earlier kernels, the next
+// sequence.  What is left is a chain of latencies: P is loaded with the first queries, the next
 // sequence's queries during this one's projection, and after it each head is one warp's business.  64 registers
 // leave room for an attention block, or a second block of this kernel, beside this one.
 __device__ __forceinline__ void mma_f64(double2& d, double a, double b) {
@@ -149,16 +149,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   // fragment of the instruction: row (head) or column lane / 4; input dims 8 s + 2 (lane % 4), + 1 for step 2 s, 2 s + 1
   const int fr = lane >> 2, fk = 2 * (lane & 3);
-  // P is read before the wait on the previous kernel: whatever may still run then does not write it
-  float pr[D / 4];
-  {
-    const float* Pg = p.P + (size_t)g * D * D + (size_t)fk * D + 8 * w + fr;
-#pragma unroll
-    for (int i = 0; i < D / 4; i += 2) {
-      pr[i] = __ldg(Pg + 4 * i * D);
-      pr[i + 1] = __ldg(Pg + 4 * i * D + D);
-    }
-  }
+  prefetch_head(p.P + (size_t)g * D * D, tid, kSelThreads);
   for (int i = tid; i < kMaxG * (D + 8); i += kSelThreads) qd[0][i] = 0.0;
   pdl_wait();
   pdl_launch_dependents();
@@ -176,6 +167,15 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
     }
   };
   fetch(blockIdx.x * group);
+  float pr[D / 4];
+  {
+    const float* Pg = p.P + (size_t)g * D * D + (size_t)fk * D + 8 * w + fr;
+#pragma unroll
+    for (int i = 0; i < D / 4; i += 2) {
+      pr[i] = __ldg(Pg + 4 * i * D);
+      pr[i + 1] = __ldg(Pg + 4 * i * D + D);
+    }
+  }
 #pragma unroll 1
   for (int b = blockIdx.x * group; b < b_end; ++b) {
     const int u = b * c.Hkv + g;

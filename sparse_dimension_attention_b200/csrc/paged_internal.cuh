@@ -112,6 +112,13 @@ __device__ __forceinline__ F rotated(const float* row, int i, const float* cs, i
   return first ? x * c - y * s : x * c + y * s;
 }
 
+// Has P of one head (64 KB) brought to L2, 128 bytes a thread and turn.  Before the wait on the previous kernel: that
+// kernel may be what writes P, so it is read only after the wait, which alone makes the writes visible.
+__device__ __forceinline__ void prefetch_head(const float* P, int tid, int nthreads) {
+  for (int i = tid; i < kHeadDim * kHeadDim / 32; i += nthreads)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(P + 32 * i));
+}
+
 __device__ __forceinline__ void report_arg(const PagedView& c) { record_status(c.ctrl, AQUA_ERR_ARG); }
 
 }  // namespace aqua

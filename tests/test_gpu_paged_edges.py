@@ -264,3 +264,51 @@ def test_decode_queries_at_the_ends_of_the_range(exponent):
     ref = oracle_decode(snap(cache), lens, q, P32, k, None, False, "f32")
     np.testing.assert_array_equal(got["sel"], ref["sel"])
     assert np.max(rel_err_rows(got["out"], ref["out"])) <= 1e-5
+
+
+# ------------------------------------------------------------------ P written by the kernel just before
+
+@pytest.mark.parametrize("what", ["step", "tiles", "decode"])
+def test_a_projection_that_the_kernel_before_writes(what):
+    """P computed on the same stream right before the call, another one each time, with the append or step before still
+    on the GPU: each call reads its own P."""
+    Hkv, Hq, page, m, k = 2, 8, 64, 128, 128
+    rng = np.random.default_rng(98)
+    _, P32 = calib_P(Hkv)
+    base = tdev(P32)
+    n = 600 if what == "tiles" else 2
+    x, v = tdev(rows_of(rng, n, Hkv, "f32", 0.3)), tdev(rows_of(rng, n, Hkv, "f32", 0.3))
+    q = tdev(rows_of(rng, 2, Hq, "f32", 0.3))
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n // 2, n], dtype=torch.int32, device="cuda") if what == "tiles" else None
+    ln = torch.tensor([500, 77], dtype=torch.int32, device="cuda")
+    turns = [(1.0, 0), (-2.0, 5), (0.5, 40), (4.0, 99)] * 3
+    Ps = [(f * base.roll(r, 2)).contiguous() for f, r in turns]
+
+    def call(cache, P, ws, out):
+        if what == "decode":
+            aq.aqua_paged_decode_attn(cache.desc, q, ln, P, Hq, k, out, ws)
+        else:
+            aq.aqua_paged_append(cache.desc, x, v, start, P, cu_new=cu)
+
+    def fresh():
+        cache = make_cache(2, Hkv, page, m, 8, seed=99)
+        return cache, torch.empty(aq.aqua_paged_decode_workspace_size(cache.desc, Hq), dtype=torch.uint8, device="cuda"), \
+            torch.zeros(2, Hq, 128, device="cuda")
+
+    caches, want, got = [fresh() for _ in turns], [], []
+    for P, (c, ws, out) in zip(Ps, caches):
+        torch.cuda.synchronize()
+        call(c, P, ws, out)
+        torch.cuda.synchronize()
+        want.append((c.k_pages.clone(), c.k_scale.clone(), out.clone()))
+    caches = [fresh() for _ in turns]
+    P = torch.empty_like(base)
+    torch.cuda.synchronize()
+    for (f, r), (c, ws, out) in zip(turns, caches):
+        torch.mul(base.roll(r, 2), f, out=P)
+        call(c, P, ws, out)
+    torch.cuda.synchronize()
+    for w, (c, ws, out) in zip(want, caches):
+        for a, b in zip(w, (c.k_pages, c.k_scale, out)):
+            assert torch.equal(a, b)
