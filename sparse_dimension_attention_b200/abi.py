@@ -48,6 +48,7 @@ class AquaError(RuntimeError):
 
 class aqua_cache(ctypes.Structure):
     """Mirror of struct aqua_cache in include/aqua.h."""
+    device = None   # index of the GPU its buffers are on (-1: host); set by the Python objects, not part of the C struct
     _fields_ = [
         ("k_proj", c_void_p), ("v", c_void_p), ("len", c_void_p), ("n_abs", c_void_p),
         ("pos", c_void_p), ("score", c_void_p), ("ctrl", c_void_p),
@@ -58,6 +59,7 @@ class aqua_cache(ctypes.Structure):
 
 class aqua_paged_cache(ctypes.Structure):
     """Mirror of struct aqua_paged_cache in include/aqua.h."""
+    device = None   # as in aqua_cache
     _fields_ = [
         ("k_pages", c_void_p), ("v_pages", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
         ("block_table", c_void_p), ("ctrl", c_void_p),
@@ -281,12 +283,16 @@ def _rows(t, heads: int, what: str) -> tuple[int, int]:
     return (row if n > 1 else 0), (head if heads > 1 else 0)
 
 
-def _one_device(t, *others) -> int:
-    """Index of the one device all tensors of a call are on."""
+def _one_device(caches, t, *others) -> int:
+    """Index of the one device all tensors and caches of a call are on (a descriptor made by hand does not say)."""
     dev = t.get_device()
     for o in others:
         if o is not None and o.get_device() != dev:
             raise AquaError(AQUA_ERR_ARG, f"tensors on device {o.get_device()} and {dev} in one call")
+    for c in caches:
+        if c.device is not None and c.device != dev:
+            where = f"on device {c.device}" if c.device >= 0 else "on the host"
+            raise AquaError(AQUA_ERR_ARG, f"a cache {where} and tensors on device {dev} in one call")
     return dev
 
 
@@ -308,7 +314,15 @@ def _rope(rope):
 
 def aqua_paged_status(cache: aqua_paged_cache, stream=None) -> int:
     out = c_int(0)
-    _check(load_library().aqua_paged_status(ctypes.byref(cache), ctypes.byref(out), _stream(stream)))
+    dev = cache.device
+    if dev is None:
+        _check(load_library().aqua_paged_status(ctypes.byref(cache), ctypes.byref(out), _stream(stream)))
+        return out.value
+    if dev < 0:
+        raise AquaError(AQUA_ERR_ARG, "the cache is on the host")
+    if torch is None:
+        _torch()
+    _call(load_library().aqua_paged_status, dev, stream, ctypes.byref(cache), ctypes.byref(out))
     return out.value
 
 
@@ -326,7 +340,7 @@ def aqua_paged_append(cache: aqua_paged_cache, k_new, v_new, start, P, cu_new=No
     if cu_new is not None:
         _want(cu_new, (cache.B + 1,), torch.int32, "cu_new")
     _call((_lib or load_library()).aqua_paged_append,
-          _one_device(k_new, v_new, start, P, cu_new, rope and rope.cos_sin), stream, ctypes.byref(cache),
+          _one_device((cache,), k_new, v_new, start, P, cu_new, rope and rope.cos_sin), stream, ctypes.byref(cache),
           k_new.data_ptr(), v_new.data_ptr(), io, ks, kh, vs, vh, k_new.shape[0], start.data_ptr(), _ptr(cu_new),
           P.data_ptr(), _rope(rope))
 
@@ -357,7 +371,7 @@ def aqua_paged_decode_attn(cache: aqua_paged_cache, q, len, P, Hq: int, k: int, 
     if not workspace.is_contiguous():
         raise AquaError(AQUA_ERR_ARG, "workspace must be contiguous")
     _call((_lib or load_library()).aqua_paged_decode_attn,
-          _one_device(q, len, P, out, workspace, sel_out, qproj_out, lse_out, rope and rope.cos_sin), stream,
+          _one_device((cache,), q, len, P, out, workspace, sel_out, qproj_out, lse_out, rope and rope.cos_sin), stream,
           ctypes.byref(cache), len.data_ptr(), q.data_ptr(), io, qs, qh, P.data_ptr(), _rope(rope), Hq, k, scale,
           out.data_ptr(), od, _ptr(sel_out), _ptr(qproj_out), _ptr(lse_out), workspace.data_ptr(),
           workspace.nbytes)
@@ -370,5 +384,5 @@ def aqua_paged_gather(cache: aqua_paged_cache, len, dst: aqua_cache, max_len: in
     _want(len, (cache.B,), torch.int32, "len")
     if seq_idx is not None:
         _want(seq_idx, (dst.B,), torch.int32, "seq_idx")
-    _call((_lib or load_library()).aqua_paged_gather, _one_device(len, seq_idx), stream, ctypes.byref(cache),
+    _call((_lib or load_library()).aqua_paged_gather, _one_device((cache, dst), len, seq_idx), stream, ctypes.byref(cache),
           len.data_ptr(), _ptr(seq_idx), ctypes.byref(dst), max_len)

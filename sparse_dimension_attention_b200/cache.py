@@ -38,6 +38,7 @@ class AquaCache:
             self.pos.data_ptr() if h2o else None, self.score.data_ptr() if h2o else None,
             self.ctrl.data_ptr(), B, Hkv, d, d_store, Tcap, 0,
             abi.AQUA_BF16 if dtype == torch.bfloat16 else abi.AQUA_F32, self.dv_store)
+        self.desc.device = self.len.get_device()
 
     @property
     def max_len(self) -> int:

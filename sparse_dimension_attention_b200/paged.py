@@ -54,6 +54,7 @@ class AquaPagedCache:
         self.desc = abi.aqua_paged_cache(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
             self.ctrl.data_ptr(), B, Hkv, d, d_store, page_size, n_pages, max_pages, abi.AQUA_E4M3)
+        self.desc.device = k_pages.get_device()
 
 
 class AquaRope:
