@@ -989,7 +989,7 @@ template <typename T>
 __global__ void __launch_bounds__(kStepThreads) paged_append_step_kernel(PagedView c, AppendParams a, int group) {
   extern __shared__ __align__(16) double part[];           // [kStepSlices][group][D]
   __shared__ __align__(16) double xs[kStepGroup][D];       // rotated rows
-  __shared__ float raw[kStepGroup][D];
+  __shared__ __align__(16) float raw[kStepGroup][D];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, h = blockIdx.y;
   const int col = tid & (D - 1), sl = tid >> 7;
   constexpr int R = D / kStepSlices;

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_select_kernel(PagedView 
   static_assert(kSelThreads == 4 * D && kMaxG == 8, "eight columns a warp, eight rows an instruction");
   constexpr int kEach = kMaxG * D / kSelThreads;      // elements of the group's queries a thread
   __shared__ __align__(16) double qd[kMaxG][D + 8];   // rotated rows; the pad keeps the fragments' reads apart
-  __shared__ float raw[kMaxG][D], qs[kMaxG][D];
+  __shared__ __align__(16) float raw[kMaxG][D], qs[kMaxG][D];
   __shared__ uint32_t kept[kMaxG][4];
   __shared__ int before;
   const int g = blockIdx.y;
