@@ -1179,13 +1179,16 @@ constexpr int kMergeWarps = 8;
 constexpr int kMergeFew = 8;
 constexpr int kMaxPieces = 2048;
 constexpr int kPiecesPerBlock = 2;         // a first piece and a later one
+// At most that many units of kMaxG heads for each block of the merge, whether a warp or the block takes them.
+constexpr int kMaxRedo = kPiecesPerBlock * kMaxG * 2;
 
 // A NaN code in a dimension that a head left out makes its score on the tensor cores NaN (the query's factor there is
 // 0, and the rows come with every dimension that a head of the group kept).  So a head with a NaN that its query does
 // not bring is formed again here, by one warp over the dimensions it kept: a token a lane for the scores, four dims of
-// the output a lane for the values.  A NaN in a kept dimension shows again and ends the work.  Rare, and slow: 32
-// tokens a time.
-__device__ __noinline__ void form_again(const PagedView& c, const DecodeP& p, int G, int u, int hh, int cols, int stride, int parts) {
+// the output a lane for the values.  A NaN in a kept dimension shows again and ends the work; the first of them is
+// looked through ahead, since a row that a NaN was appended to is NaN as a whole.  Rare, and slow: one head of 131072
+// tokens 47 ms, 0.3 ms where its rows are NaN as a whole.
+__device__ __forceinline__ void form_again(const PagedView& c, const DecodeP& p, int G, int u, int hh, int cols, int stride, int parts) {
   const int lane = threadIdx.x & 31, b = u / c.Hkv, g = u % c.Hkv;
   const size_t row = (size_t)b * p.Hq + (size_t)g * G + hh;
   const float fac = p.qfac[(size_t)u * kMaxG + hh];
@@ -1199,24 +1202,41 @@ __device__ __noinline__ void form_again(const PagedView& c, const DecodeP& p, in
     kept[y] = __ballot_sync(0xffffffffu, q[32 * y] != 0);
   }
   const int n = seq_tokens(c, p, b), mask = (1 << c.page_log2) - 1;
-  float M = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int first = kept[0] ? __ffs(kept[0]) - 1 : kept[1] ? __ffs(kept[1]) + 31 : kept[2] ? __ffs(kept[2]) + 63 : __ffs(kept[3]) + 95;
+  auto page_of = [&](int t) {
+    const int pid = t < n ? __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2)) : -1;
+    return pid < c.n_pages ? pid : -1;
+  };
+  bool nan = false;
+#pragma unroll 4
+  for (int t = 16 * lane; t < n; t += 32 * 16) {                 // sixteen codes, of one page
+    const int pid = page_of(t);
+    if (pid < 0) continue;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(c.k + c.kblock(pid, g) + ((size_t)first << c.page_log2) + (t & mask)));
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) nan |= t + i < n && ((words[i >> 2] >> (8 * (i & 3))) & 0x7fu) == 0x7fu;
+  }
+  nan = __any_sync(0xffffffffu, nan);
+  float M = nan ? NAN : -INFINITY, l = nan ? NAN : 0.f;
+  float4 acc = nan ? make_float4(NAN, NAN, NAN, NAN) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int t0 = 0; t0 < n; t0 += 32) {
-    const int t = t0 + lane;
-    int pid = -1;
-    if (t < n) pid = __ldg(c.table + (size_t)b * c.max_pages + (t >> c.page_log2));
-    const bool seen = pid >= 0 && pid < c.n_pages;
+  for (int t0 = nan ? n : 0; t0 < n; t0 += 32) {
+    const int t = t0 + lane, pid = page_of(t);
+    const bool seen = pid >= 0;
     const size_t si = seen ? (size_t)pid * c.Hkv + g : 0;
     const uint8_t* key = c.k + (seen ? c.kblock(pid, g) + (t & mask) : 0);
     float s = 0.f;
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
 #pragma unroll 1
-      for (uint32_t left = kept[y]; left != 0; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        const float xi = __shfl_sync(0xffffffffu, x[y], i);
-        if (seen) s = fmaf(xi, e4m3x2_to_f32x2(key[(size_t)(i + 32 * y) << c.page_log2]).x, s);
+      for (int i0 = 0; i0 < 32; i0 += 16) {                      // sixteen loads in flight
+        uint8_t code[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          code[i] = seen && ((kept[y] >> (i0 + i)) & 1u) ? key[(size_t)(i0 + i + 32 * y) << c.page_log2] : (uint8_t)0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s = fmaf(__shfl_sync(0xffffffffu, x[y], i0 + i), e4m3x2_to_f32x2(code[i]).x, s);
       }
     }
     s = seen ? s * (fac * c.ks[si]) : -INFINITY;
@@ -1235,13 +1255,20 @@ __device__ __noinline__ void form_again(const PagedView& c, const DecodeP& p, in
     acc.x *= al; acc.y *= al; acc.z *= al; acc.w *= al;
     const float w = seen ? e * c.vs[si] : 0.f;
 #pragma unroll 1
-    for (uint32_t left = __ballot_sync(0xffffffffu, seen); left != 0; left &= left - 1) {
-      const int i = __ffs(left) - 1, pi = __shfl_sync(0xffffffffu, pid, i);
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const uint32_t v = reinterpret_cast<const uint32_t*>(c.v + c.vblock(pi, g) + (size_t)((t0 + i) & mask) * D)[lane];
-      const float2 v0 = e4m3x2_to_f32x2((uint16_t)v), v1 = e4m3x2_to_f32x2((uint16_t)(v >> 16));
-      acc.x = fmaf(wi, v0.x, acc.x); acc.y = fmaf(wi, v0.y, acc.y);
-      acc.z = fmaf(wi, v1.x, acc.z); acc.w = fmaf(wi, v1.y, acc.w);
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pi = __shfl_sync(0xffffffffu, pid, i0 + i);
+        v[i] = pi >= 0 ? reinterpret_cast<const uint32_t*>(c.v + c.vblock(pi, g) + (size_t)((t0 + i0 + i) & mask) * D)[lane] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+        const float2 v0 = e4m3x2_to_f32x2((uint16_t)v[i]), v1 = e4m3x2_to_f32x2((uint16_t)(v[i] >> 16));
+        acc.x = fmaf(wi, v0.x, acc.x); acc.y = fmaf(wi, v0.y, acc.y);
+        acc.z = fmaf(wi, v1.x, acc.z); acc.w = fmaf(wi, v1.y, acc.w);
+      }
     }
   }
 #pragma unroll
@@ -1257,7 +1284,10 @@ __device__ __noinline__ void form_again(const PagedView& c, const DecodeP& p, in
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedView c, const __grid_constant__ DecodeP p, int G, int cols, int stride, int parts) {
   __shared__ __align__(16) float sum[kMergeWarps][D];
   __shared__ float2 ml[kMergeWarps];
+  __shared__ int redo[kMaxRedo], n_redo;   // heads to form again among this block's: unit * kMaxG + head
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  if (tid == 0) n_redo = 0;
+  __syncthreads();
   pdl_wait();
   int4 sp = p.split[blockIdx.x / G];       // along with their number: the list has room for more than the blocks
   const int n_jobs = p.ctl[1] * G, n_again = p.ctl[2];
@@ -1296,7 +1326,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
       acc.z = fmaf(v[i].z, f, acc.z); acc.w = fmaf(v[i].w, f, acc.w);
     }
     if (odd(L, s1.x, hh)) {
-      form_again(c, p, G, s1.x, hh, cols, stride, parts);
+      if (lane == 0) redo[atomicAdd(&n_redo, 1)] = s1.x * kMaxG + hh;
       continue;
     }
     const size_t row = (size_t)(s1.x / c.Hkv) * p.Hq + (size_t)(s1.x % c.Hkv) * G + hh;
@@ -1353,7 +1383,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
 #pragma unroll
     for (int z = 0; z < kMergeWarps; ++z) all += ml[z].y;
     if (odd(all, sp.x, hh)) {
-      if (w == 0) form_again(c, p, G, sp.x, hh, cols, stride, parts);
+      if (tid == 0) redo[atomicAdd(&n_redo, 1)] = sp.x * kMaxG + hh;
     } else if (tid < D) {
       float top = -INFINITY;
 #pragma unroll
@@ -1372,9 +1402,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     }
     __syncthreads();
   }
+  // formed again at the end, in one place: calls among the merges cost every step 1 us
+  __syncthreads();
+  const int mine = n_redo, n_jobs_again = mine + max(0, (n_again - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x);
 #pragma unroll 1
-  for (int job = blockIdx.x * kMergeWarps + w; job < n_again; job += gridDim.x * kMergeWarps)
-    form_again(c, p, G, p.again[job] / kMaxG, p.again[job] % kMaxG, cols, stride, parts);
+  for (int i = w; i < n_jobs_again; i += kMergeWarps) {
+    const int what = i < mine ? redo[i] : p.again[blockIdx.x + (i - mine) * gridDim.x];
+    form_again(c, p, G, what / kMaxG, what % kMaxG, cols, stride, parts);
+  }
 }
 
 // ---------------------------------------------------------------- host side

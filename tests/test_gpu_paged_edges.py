@@ -7,7 +7,7 @@ import torch
 import sparse_dimension_attention_b200 as aq
 from oracle import paged_oracle as PO
 from aqua_testlib import calib_P, rel_err_rows, tdev
-from test_gpu_paged import DT, check_append, make_cache, oracle_decode, rows_of, run_paged_decode, snap
+from test_gpu_paged import DT, check_append, make_cache, oracle_decode, rows_of, run_paged_decode, snap, torch_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -248,6 +248,37 @@ def test_decode_nan_keys_in_dimensions_that_a_head_left_out(od):
     np.testing.assert_array_equal(np.isnan(got["lse"]), want)
     assert np.max(rel_err_rows(got["out"][~want], ref["out"][~want])) <= (2e-3 if od == "bf16" else 1e-5)
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+@pytest.mark.parametrize("n", [900, 20000, 131072])
+def test_decode_nan_keys_left_out_in_a_unit_of_many_parts(n):
+    """The same where a unit is shared by few and by many blocks: one head left the NaN out, one kept it, one more has a
+    whole row of NaN only behind the length."""
+    page, m, k, G = 64, 96, 40, 3
+    rng = np.random.default_rng(101)
+    cache = make_cache(1, 1, page, m, -(-(n + 1) // page), seed=102)
+    table = cache.block_table[0].tolist()
+    for t in rng.integers(0, n, 5):
+        cache.k_pages[table[t // page], 0, 90, int(t) % page] = 0x7F
+    cache.k_pages[table[n // page], 0, :, n % page] = 0xFF
+    q = rng.normal(size=(1, G, 128)) * 0.1 + 1.0
+    q[0, :, 90] = [0.01, 3.0, -0.01]
+    qt = tdev(q)
+    P = torch.eye(128, device="cuda")[None].contiguous()
+    for od, tol in (("f32", 1e-5), ("bf16", 4e-3)):
+        out = torch.empty(1, G, 128, dtype=DT[od], device="cuda")
+        lse = torch.empty(1, G, device="cuda")
+        ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, G),), 0xFF, dtype=torch.uint8, device="cuda")
+        aq.aqua_paged_decode_attn(cache.desc, qt, torch.tensor([n], dtype=torch.int32, device="cuda"), P, G, k, out, ws, lse_out=lse)
+        clean = cache.k_pages.clone()
+        codes = clean.view(torch.float8_e4m3fn).float()
+        cache.k_pages.masked_fill_(codes.isnan(), 0)
+        ref = torch_decode(cache, qt, [n], P, k)
+        cache.k_pages.copy_(clean)
+        assert bool(out[0, 1].isnan().all()) and bool(lse[0, 1].isnan())
+        for h in (0, 2):
+            assert float((out[0, h].double() - ref[0, h]).norm() / ref[0, h].norm()) <= tol
+            assert bool(lse[0, h].isfinite())
 
 
 @pytest.mark.parametrize("exponent", [100, 118, 126, -100, -118])
