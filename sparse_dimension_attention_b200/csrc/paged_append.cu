@@ -287,13 +287,14 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
 //
 // A tile is 128 slots of a sequence, aligned, so whole pages; persistent blocks,
 // one an SM, each of one head, share the tiles.  k~ = x P on tcgen05 with
-// both factors split into two f16 parts (x_l P_h + x_h P_l + x_h P_h, f32
+// both factors split into two f16 parts (x_l P_l + x_l P_h + x_h P_l + x_h P_h, f32
 // accumulation): rows and P are first brought to [2^10, 2^11) by powers of two,
-// so the parts hold 22 bits and the dropped product is below 2^-22 of a term.
-// The tensor cores cut every sum they extend off to 24 bits, which makes one chain
-// of 24 products 2.3e-7 off (2-norm; an f32 sum of 128 terms 2.0e-7, exact sums of
-// the same parts 0.7e-7).  So two accumulators of 64 input dims each, the small
-// products first, added in f32: 1.5e-7.
+// so the parts hold 22 bits.  The tensor cores cut every sum they extend off to 24
+// bits, which makes one chain of a row's products 2.3e-7 off (2-norm; an f32 sum of
+// 128 terms 2.0e-7).  So two accumulators of 64 input dims each, the small products
+// first, added in f32: of 40 calls of 701 f32 tokens and 4 heads 70 codes fall on
+// the other side of a tie (92 without x_l P_l, which costs 1 %; 115 with the rows
+// projected by a library's f32 product).
 //
 // What bounds it is the arithmetic around the products (some 20 instructions an
 // element), so the roles overlap: warps 0-7 rotate, normalise and split the rows
@@ -731,9 +732,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t xa = smem_u32(sX) + buf * 2 * kPart, pa = smem_u32(sP);
 #pragma unroll
-        for (int pr = 0; pr < 3; ++pr) {     // x_l P_h, x_h P_l, x_h P_h: the small ones first
-          const uint64_t ad = desc_sw128(xa + (pr == 0 ? kPart : 0), 16);
-          const uint64_t bd = desc_sw128(pa + (pr == 1 ? kPart : 0), kTile * 128);
+        for (int pr = 0; pr < 4; ++pr) {     // x_l P_l, x_l P_h, x_h P_l, x_h P_h: the small ones first
+          const uint64_t ad = desc_sw128(xa + (pr < 2 ? kPart : 0), 16);
+          const uint64_t bd = desc_sw128(pa + (pr % 2 == 0 ? kPart : 0), kTile * 128);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             mma_f16(tmem + buf * 2 * D + (ks >> 2) * D, ad + (uint64_t)(((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4),

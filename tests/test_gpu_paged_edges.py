@@ -49,7 +49,7 @@ def test_decode_of_a_batch_without_tokens(B, Hq, Hkv, od, rejected):
 F32_MAX = float(np.finfo(np.float32).max)
 
 
-@pytest.mark.parametrize("n,io", [(300, "f32"), (300, "bf16"), (20, "f32")])       # tensor-core tiles, CUDA cores
+@pytest.mark.parametrize("n,io", [(300, "f32"), (300, "bf16"), (20, "f32")])                    # tensor-core tiles
 def test_append_projections_past_f32(n, io):
     """Finite rows whose projection leaves f32 in one dimension: the finite ones set the page's scale, the
     others saturate or keep their own code, rows beside them (of the same warp too) are what they would be."""
@@ -87,6 +87,25 @@ def test_append_projections_past_f32(n, io):
             np.testing.assert_array_equal(PO.e4m3_decode(a["v_pages"][pid, h][:x.shape[0]]),
                                           PO.e4m3_round(v[rows, h] / float(a["v_scale"][pid, h])))
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+@pytest.mark.parametrize("n", [300, 20, 10])                            # tensor-core tiles, CUDA cores
+def test_append_products_of_low_bits(n):
+    """x0 = P0 = 1 + l, x1 = -1, P1 = 1 + 2 l with l just below half a step of f16 at 1: all that is left of the sum is
+    l^2 = 2^-22, the product of what f16 leaves of both factors.  f32 sums may cut 2^-24 off twice on the way."""
+    Hkv, page, m = 8, 64, 128
+    l = 2.0 ** -11 - 2.0 ** -22
+    k = np.zeros((n, Hkv, 128))
+    k[:, :, 0], k[:, :, 1] = 1 + l, -1
+    P32 = np.zeros((Hkv, 128, 128), dtype=np.float32)
+    P32[:, 0], P32[:, 1] = 1 + l, 1 + 2 * l
+    assert (k == k.astype(np.float32)).all() and P32[0, 1, 0] == 1 + 2 * l
+    cache = make_cache(1, Hkv, page, m, -(-n // page), seed=85)
+    aq.aqua_paged_append(cache.desc, tdev(k), tdev(k), torch.zeros(1, dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    a = snap(cache)
+    kk, _ = PO.read_sequence(a["k_pages"], a["v_pages"], a["k_scale"], a["v_scale"], a["block_table"][0], n)
+    assert np.abs(kk - l * l).max() <= 2.0 ** -23 + 2.0 ** -4 * l * l
 
 
 def test_append_runs_that_share_rows():
