@@ -167,6 +167,10 @@ __device__ __forceinline__ float page_scale(float amax, float old, int fill) {
   return fill > 0 ? fmaxf(old, s) : s;
 }
 
+// Rows are rotated and summed times 2^-16, so that a sum of large numbers is an infinity only where the result is one;
+// exact for all above 2^-110, and what is smaller has the code 0.
+constexpr float kDown = 1.f / 65536.f;
+
 // A block takes page segments of one KV head.  A thread holds 16 rows x 4 columns of
 // P in registers, so P is read once; eight tokens at a time are projected (warp w
 // sums input dims 16w .. 16w+15) and their eight partial sums added in order.
@@ -203,6 +207,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
       if (w < nt) {
         float f[4];
         load4<T>(kr + (size_t)(t0 + w) * a.ks.row + 4 * lane, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] *= kDown;
         *reinterpret_cast<float4*>(raw + w * D + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
         __syncwarp();
         if (a.rope.cs != nullptr) {
@@ -235,8 +241,10 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
           y[0] += q.x; y[1] += q.y; y[2] += q.z; y[3] += q.w;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
+          y[e] *= 1.f / kDown;
           if (4 * lane + e < c.m) kmax = fmaxf(kmax, finite_abs(y[e]));
+        }
         *reinterpret_cast<float4*>(kt + (size_t)(t0 + w) * D + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
       }
       __syncthreads();

@@ -49,7 +49,7 @@ def test_decode_of_a_batch_without_tokens(B, Hq, Hkv, od, rejected):
 F32_MAX = float(np.finfo(np.float32).max)
 
 
-@pytest.mark.parametrize("n,io", [(300, "f32"), (300, "bf16"), (20, "f32")])                    # tensor-core tiles
+@pytest.mark.parametrize("n,io", [(300, "f32"), (300, "bf16"), (20, "f32"), (10, "f32")])     # tensor-core tiles, CUDA cores
 def test_append_projections_past_f32(n, io):
     """Finite rows whose projection leaves f32 in one dimension: the finite ones set the page's scale, the
     others saturate or keep their own code, rows beside them (of the same warp too) are what they would be."""
