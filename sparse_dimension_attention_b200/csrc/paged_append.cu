@@ -167,8 +167,8 @@ __device__ __forceinline__ float page_scale(float amax, float old, int fill) {
   return fill > 0 ? fmaxf(old, s) : s;
 }
 
-// Rows are rotated and summed times 2^-16, so that a sum of large numbers is an infinity only where the result is one;
-// exact for all above 2^-110, and what is smaller has the code 0.
+// Rows are rotated and summed times 2^-16 (unless they are brought to one size anyway), so that a sum of large numbers
+// is an infinity only where the result is one; exact for all above 2^-110, and what is smaller has the code 0.
 constexpr float kDown = 1.f / 65536.f;
 
 // A block takes page segments of one KV head.  A thread holds 16 rows x 4 columns of
@@ -688,12 +688,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int i = 16 * j8 + e;
-            float v = live ? Elem<T>::load(src + i) : 0.f;
+            float v = live ? Elem<T>::load(src + i) * kDown : 0.f;
             if (live && i < rot) {
               const bool first = a.rope.interleaved ? (i & 1) == 0 : i < half;
               const int j = a.rope.interleaved ? i >> 1 : (first ? i : i - half);
               const int o = a.rope.interleaved ? i ^ 1 : (first ? i + half : i - half);
-              const float cc = __ldg(cs + j), ss = __ldg(cs + half + j), z = Elem<T>::load(src + o);
+              const float cc = __ldg(cs + j), ss = __ldg(cs + half + j), z = Elem<T>::load(src + o) * kDown;
               v = first ? v * cc - z * ss : v * cc + z * ss;
             }
             x[e] = v;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) paged_append_tile_kernel(Page
           for (int e = 0; e < 16; ++e) x[e] *= up;
         }
         if (pass == 0 && t >= 2) tile_wait(&ms.x_free[buf], ((t - 2) >> 1) & 1, ms, c.ctrl);
-        if (j8 == 0) ms.unit[t & 3][r] = undo * p_undo;
+        if (j8 == 0) ms.unit[t & 3][r] = undo * p_undo * (MODE == kAnyRot ? 1.f / kDown : 1.f);
         uint32_t hw[8], lw[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

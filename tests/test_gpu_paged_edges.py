@@ -7,7 +7,7 @@ import torch
 import sparse_dimension_attention_b200 as aq
 from oracle import paged_oracle as PO
 from aqua_testlib import calib_P, rel_err_rows, tdev
-from test_gpu_paged import DT, check_append, make_cache, oracle_decode, rows_of, run_paged_decode, snap, torch_decode
+from test_gpu_paged import DT, check_append, make_cache, oracle_decode, rope_of, rows_of, run_paged_decode, snap, torch_decode
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +87,32 @@ def test_append_projections_past_f32(n, io):
             np.testing.assert_array_equal(PO.e4m3_decode(a["v_pages"][pid, h][:x.shape[0]]),
                                           PO.e4m3_round(v[rows, h] / float(a["v_scale"][pid, h])))
     assert aq.aqua_paged_status(cache.desc) == aq.AQUA_OK
+
+
+@pytest.mark.parametrize("rope", [(128, False), (64, True), (36, False), (6, True)])
+@pytest.mark.parametrize("n", [300, 10, 1])                                         # tensor-core tiles, CUDA cores, one token
+def test_append_large_rows_rotated(n, rope):
+    """Finite rows near the largest f32 number whose rotated entries may leave f32 while what they project to does not."""
+    Hkv, page, m = 8, 64, 128
+    rng = np.random.default_rng(86)
+    _, P32 = calib_P(Hkv)
+    P = P32.astype(np.float64)
+    cache = make_cache(1, Hkv, page, m, -(-n // page) + 1, seed=87)
+    r, rn, inter = rope_of(rope)
+    k, v = rows_of(rng, n, Hkv, "f32"), rows_of(rng, n, Hkv, "f32")
+    rot, start = rope[0], 7
+    k[::3] = 0
+    for i in range(0, n, 3):                  # one rotated pair of each such row: only its rotated entries may leave f32
+        j = int(rng.integers(0, rot // 2))
+        k[i, :, [2 * j, 2 * j + 1] if inter else [j, j + rot // 2]] = np.float64(np.float32(3.2e38)) * rng.choice([-1, 1], (2, 1))
+    kr = PO.rotate(k, np.arange(start, start + n), rn, inter)
+    kt, err = np.einsum("nhi,hij->nhj", kr, P), 132 * 2.0 ** -24 * np.einsum("nhi,hij->nhj", np.abs(kr), np.abs(P))
+    assert np.all(np.abs(kt) + err < F32_MAX) and (n == 1 or np.abs(kr).max() > F32_MAX)
+    cu = None if n == 1 else torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    before = snap(cache)
+    aq.aqua_paged_append(cache.desc, tdev(k), tdev(v), torch.tensor([start], dtype=torch.int32, device="cuda"), tdev(P32),
+                         cu_new=cu, rope=r)
+    check_append(cache, before, k, v, P32, [start], None if n == 1 else [0, n], rn, inter)
 
 
 @pytest.mark.parametrize("n", [300, 20, 10])                            # tensor-core tiles, CUDA cores
