@@ -343,8 +343,9 @@ AQUA_API int aqua_selftest_wait_timeout(aqua_cache* cache, unsigned long long li
  *                                        inside a page, so that a decode step reads
  *                                        only the rows its heads kept
  *   v_pages [n_pages][Hkv][page_size][d] e4m3  unprojected values, token-major
- *   k_scale, v_scale [n_pages][Hkv]      f32   positive; aqua_paged_append gives powers
- *                                        of two.  Not read for pages without tokens.
+ *   k_scale, v_scale [n_pages][Hkv]      f32   positive, v_scale 2^-60 or more;
+ *                                        aqua_paged_append gives powers of two from
+ *                                        there on.  Not read for pages without tokens.
  *   block_table [B][max_pages]           int32 page of every page_size tokens; entries
  *                                        past a sequence's length are not read
  *   ctrl    [AQUA_CTRL_WORDS]            int32 control words, zero at creation; word 0 is

@@ -1,7 +1,7 @@
 // Append to the paged 8-bit cache: rotate, project, quantise, scatter.
 //
 // For every new token at slot t of its sequence and KV head g:
-//   k~ = rope(k, t) P[g][:, :m]                       (f32)
+//   k~ = rope(k, t) P[g][:, :m]                       (f64, f32 or two f16 parts of each factor: see the kernels)
 //   s  = smallest power of two with max |x| <= 448 s over the values appended to the page,
 //        or the page's own scale if that is larger and the page holds tokens already
 //   code = e4m3(x / s);  the page's older codes are re-coded by s_old / s when s grew
@@ -122,7 +122,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
   f[0] = bf16lo(w.x); f[1] = bf16hi(w.x); f[2] = bf16lo(w.y); f[3] = bf16hi(w.y);
 }
 
-// four codes times ratio, nearest even; bytes whose bit in `keep` is clear stay as they are
+// four codes times ratio, nearest even; bytes that byte_mask leaves out stay as they are
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio, uint32_t byte_mask) {
   const float2 a = e4m3x2_to_f32x2((uint16_t)(w & 0xffffu)), b = e4m3x2_to_f32x2((uint16_t)(w >> 16));
   const uint32_t r = f32x4_to_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_run_kernel(PagedView c,
 // values, one lane issues the products.  Operands and accumulators are double.
 // The loops are kept short (rolled over 32 rows or 32 columns): unrolled, the
 // roles together were 122 KB of code and mostly waited for instructions.
-// Measured: 8 ragged prompts of 16384 tokens together, 8 heads, bf16: 61 us (the
-// bytes alone: 17), 5.5 us a tile and SM, most of it the row warps'.
+// Measured: 8 ragged prompts of 16384 tokens together, 8 heads: bf16 64 us (the
+// bytes alone: 17), f32 72 us (27); 5.5 us a tile and SM, most of it the row warps'.
 constexpr int kTile = 128;
 constexpr int kRowThreads = 256, kKeyThreads = 128, kValThreads = 256;
 constexpr int kKeyWarp0 = kRowThreads / 32, kValWarp0 = kKeyWarp0 + kKeyThreads / 32;
@@ -988,7 +988,7 @@ int launch_tiles(const PagedView& c, const AppendParams& a, cudaStream_t st) {
 // registers and kept there as f64, whose
 // 64 multiply-adds a cycle and SM are enough here; the sums are then exact to f32
 // rounding, so that a code differs from the exact one only on a tie.  Warp t
-// writes token t.  One sequence 4.1 us, 256 of 8 heads 10.3 us, launches replayed
+// writes token t.  One sequence 4.8 us, 256 of 8 heads 11.0 us, launches replayed
 // from a graph.
 constexpr int kStepThreads = 512;
 constexpr int kStepGroup = 16;

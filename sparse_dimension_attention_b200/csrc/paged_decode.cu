@@ -46,12 +46,14 @@
 // two key and four value buffers of 16 KB, two blocks an SM.  The first tiles are
 // fetched while the selection still runs, with all their key rows.
 // A piece that starts or ends inside a (b, g) leaves (M, l, O); paged_merge_kernel
-// adds the parts in the order of the tokens.  Which block took a piece changes
+// adds the parts in the order of the tokens, and forms those heads again that a NaN
+// key in a dimension they left out made NaN.  Which block took a piece changes
 // nothing, so results do not depend on timing.
 //
-// Measured, three launches replayed from a graph: 131072 tokens x 8 heads 56 us
-// (268 MB of rows a head kept: 4.7 TB/s), 32 sequences of up to 32768 tokens, 8
-// heads of 8 queries, 181 to 192 us (4.9 TB/s), 8 x 8192 tokens 37 us.  With up to
+// Measured, three launches replayed from a graph: 131072 tokens x 8 heads 58 us
+// (268 MB of rows a head kept: 4.6 TB/s), 32 sequences of up to 32768 tokens, 8
+// heads of 8 queries, 190 to 204 us (4.6 to 5 TB/s), 8 x 8192 tokens 39 us; with f32
+// outputs 63, 329 and 44 us.  With up to
 // four heads a group the middle of a job is bound by memory (1.5 us a tile and
 // block, two blocks an SM), with eight by the softmax warps' chain of a tile; to
 // that come 9 us until the selection is done and the first scores are there,
