@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 #pragma unroll
           for (int i = CC::QPARTS - 2; i >= 0; --i) s = fmaf(s, 1.f / 16.f, v[hl * STR + i]);
           x[h] = seen ? fmaf(s, fac[h] * ksc, lv) : -INFINITY;
-          raise |= h < G && x[h] > ref[h] + kLazy;
+          raise |= h < G && x[h] - ref[h] > kLazy;     // the difference is exact where p could get too large
         }
       }
       // one thread decides for all whether an abort ends the work here

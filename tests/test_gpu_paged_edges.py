@@ -388,3 +388,24 @@ def test_a_projection_that_the_kernel_before_writes(what):
     for w, (c, ws, out) in zip(want, caches):
         for a, b in zip(w, (c.k_pages, c.k_scale, out)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+@pytest.mark.parametrize("size,rise", [(s, r) for s in (24.3, 25.3, 26.3, 30.0) for r in (2.0, 4.0, 8.0, 12.0)])
+def test_decode_scores_so_large_that_f32_steps_show(size, rise, od):
+    """Scores around 2^size (in powers of two) that rise by about one step of f32 from tile to tile: whatever the
+    weights are, all values are 1, and so is the output."""
+    page, m, k, G, tiles = 128, 16, 2, 1, 40
+    codes = [0x38 + i for i in range(tiles)]                                   # 1, 1.125, ... in dimension 1, one a tile
+    ck = torch.zeros(tiles, 1, m, page, dtype=torch.uint8)
+    ck[:, 0, 0] = 0x78                                                        # 256 in dimension 0
+    for i, c in enumerate(codes):
+        ck[i, 0, 1] = c
+    cv = torch.full((tiles, 1, page, 128), 0x38, dtype=torch.uint8)
+    cache = pooled(1, 64, np.arange(tiles), ck, cv)
+    step = 2.0 ** (int(size) - 23)
+    q = torch.zeros(1, G, 128)
+    q[0, :, 0] = 2.0 ** size / 256 * 0.6931471805599453 * 128 ** 0.5
+    q[0, :, 1] = rise * step * 128 ** 0.5
+    got, lse = decode_pooled(cache, q.cuda(), tiles * page, k, od)
+    assert bool(((got - 1).abs() <= (2.0 ** -8 if od == "bf16" else 1e-5)).all()) and bool(lse.isfinite().all())
