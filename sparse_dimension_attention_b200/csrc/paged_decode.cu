@@ -122,7 +122,8 @@ __device__ __forceinline__ void store_out_elem(const DecodeP& p, size_t i, float
 
 // result of a softmax sum: no visible token gives 0 and -inf, NaN stays
 __device__ __forceinline__ float normalised(float O, float L) { return L == 0.f ? 0.f : O / L; }
-__device__ __forceinline__ float lse_of(float M, float L) { return L == 0.f ? -INFINITY : kLn2 * (M + log2f(L)); }
+// (L held times 2^up; taken off the logarithm, since M may be so large that a difference of it would be rounded)
+__device__ __forceinline__ float lse_of(float M, float L, float up) { return L == 0.f ? -INFINITY : kLn2 * (M + (log2f(L) - up)); }
 
 // ============================================================================
 // rotation, projection, top-k
@@ -1142,14 +1143,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
           float O = head_of(v, hl);
           if (STR == 8) O += acc[h];
           const float L = (ms.red[0][h] + ms.red[1][h]) + (ms.red[2][h] + ms.red[3][h]);
-          // p was held times 2^kPScale, so M + log2 l is off by it
-          const float M = ref[h] - kPScale;
           if (ti.slot < 0) {
             store_out_elem(p, (row0 + h) * D + tid, normalised(O, L));
-            if (p.lse_out && tid == 0) p.lse_out[row0 + h] = lse_of(M, L);
+            if (p.lse_out && tid == 0) p.lse_out[row0 + h] = lse_of(ref[h], L, kPScale);
           } else {
             p.part_o[((size_t)ti.slot * G + h) * D + tid] = O;
-            if (tid == 0) p.part_ml[(size_t)ti.slot * G + h] = make_float2(M, L);
+            if (tid == 0) p.part_ml[(size_t)ti.slot * G + h] = make_float2(ref[h], L);
           }
         }
       }
@@ -1280,7 +1279,7 @@ __device__ __forceinline__ void form_again(const PagedView& c, const DecodeP& p,
   store_out_elem(p, at + 1, normalised(acc.y, l));
   store_out_elem(p, at + 2, normalised(acc.z, l));
   store_out_elem(p, at + 3, normalised(acc.w, l));
-  if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(M, l);
+  if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(M, l, 0.f);
 }
 
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedView c, const __grid_constant__ DecodeP p, int G, int cols, int stride, int parts) {
@@ -1337,7 +1336,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     store_out_elem(p, at + 1, normalised(acc.y, L));
     store_out_elem(p, at + 2, normalised(acc.z, L));
     store_out_elem(p, at + 3, normalised(acc.w, L));
-    if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(top, L);
+    if (p.lse_out && lane == 0) p.lse_out[row] = lse_of(top, L, kPScale);
   }
   // the others: a block each
 #pragma unroll 1
@@ -1400,7 +1399,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
       }
       const size_t row = (size_t)(sp.x / c.Hkv) * p.Hq + (size_t)(sp.x % c.Hkv) * G + hh;
       store_out_elem(p, row * D + tid, normalised(O, Ls));
-      if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(top, Ls);
+      if (p.lse_out && tid == 0) p.lse_out[row] = lse_of(top, Ls, kPScale);
     }
     __syncthreads();
   }

@@ -409,3 +409,28 @@ def test_decode_scores_so_large_that_f32_steps_show(size, rise, od):
     q[0, :, 1] = rise * step * 128 ** 0.5
     got, lse = decode_pooled(cache, q.cuda(), tiles * page, k, od)
     assert bool(((got - 1).abs() <= (2.0 ** -8 if od == "bf16" else 1e-5)).all()) and bool(lse.isfinite().all())
+
+
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+def test_decode_parts_of_very_large_scores_keep_their_distance(od):
+    """One unit in many parts, the scores of its first half 1.25 * 2^26 and those of its second half 8 more (in powers of
+    two, one step of f32; the scale argument makes them exact): the first half weighs 2^-8 of the second."""
+    page, m, k, n_pages = 128, 16, 2, 4000
+    ck = torch.zeros(2, 1, m, page, dtype=torch.uint8)
+    ck[:, 0, 0] = 0x78                                                        # 256
+    ck[1, 0, 1] = 0x38                                                        # 1
+    cv = torch.full((2, 1, page, 128), 0x38, dtype=torch.uint8)
+    cv[1] = 0x30                                                              # 0.5
+    scale = float(np.float32(np.log(2)))
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 1
+    cache = pooled(1, 1, np.repeat([0, 1], n_pages // 2), ck, cv)
+    q = torch.zeros(1, 1, 128)
+    q[0, 0, 0], q[0, 0, 1] = 1.25 * 2 ** 18, 8
+    out, lse = torch.empty(1, 1, 128, dtype=DT[od], device="cuda"), torch.empty(1, 1, device="cuda")
+    ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    aq.aqua_paged_decode_attn(cache.desc, q.cuda(), torch.tensor([n_pages * page], dtype=torch.int32, device="cuda"),
+                              torch.eye(128, device="cuda")[None].contiguous(), 1, k, out, ws, scale=scale, lse_out=lse)
+    want = (2.0 ** -8 + 0.5) / (1 + 2.0 ** -8)
+    assert float((out.double() - want).abs().max()) <= (want * 2.0 ** -8 if od == "bf16" else 1e-5)
+    # a sum and a product, each half a step (2^-24) off, and ln 2 in f32 (0.5 * 2^-24)
+    assert abs(float(lse) / (np.log(2) * (1.25 * 2 ** 26 + 8 + np.log2(n_pages / 2 * page * (1 + 2.0 ** -8)))) - 1) <= 2.5 * 2.0 ** -24
