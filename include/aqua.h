@@ -418,7 +418,8 @@ AQUA_API int aqua_paged_status(const aqua_paged_cache* cache, int* status_out, a
  * Appending a run at once or token by token gives the same values but for those
  * subnormals and for sums within f32 rounding of a tie: single tokens are
  * projected in f64, short runs in f32, long ones on the tensor cores with both
- * factors in two f16 parts, which is as exact as an f32 sum.
+ * factors in two f16 parts, which is as exact as an f32 sum (entries below 2^-11
+ * of their row's or of P's largest have fewer bits, 2^-35 of it).
  * A sequence whose run does not fit (or lies outside the rotation table, or
  * whose cu_new is not ascending within [0, n_tokens]) is left as it was and
  * AQUA_ERR_ARG recorded.
@@ -450,12 +451,12 @@ AQUA_API int aqua_paged_append(const aqua_paged_cache* cache, const void* k_new,
  * and a bf16 one 2^-10 for up to 500 000 tokens of a KV head in one block.
  * Codes enter the tensor cores as they are.  For an f32 output queries are held
  * to 2^-24 and weights to 2^-22 of themselves; for a bf16 one queries to 2^-16
- * (the scores and lse too) and weights to 2^-11, as in f16.  Relative to the
- * largest weight of a head, one below 2^-26 has fewer bits and one below 2^-37
- * (f32 output: 2^-49) may be lost.  A query with an infinity or NaN among its
- * kept dimensions gives NaN.  A NaN code in a key gives NaN to the heads that
- * kept its dimension and does nothing to the others (such heads are formed again
- * by a slow path).
+ * (the scores and lse too) and weights to 2^-12.  Relative to the largest weight
+ * (times its page's v_scale) of a head, one below 2^-25 has fewer bits and one
+ * below 2^-37 (f32 output: 2^-49) may be lost.  A query with an infinity or NaN
+ * among its kept dimensions gives NaN.  A NaN code in a key gives NaN to the
+ * heads that kept its dimension and does nothing to the others (such heads are
+ * formed again by a slow path).
  */
 AQUA_API size_t aqua_paged_decode_workspace_size(const aqua_paged_cache* cache, int Hq);
 AQUA_API int aqua_paged_decode_attn(const aqua_paged_cache* cache, const int32_t* len, const void* q, int io_dtype,

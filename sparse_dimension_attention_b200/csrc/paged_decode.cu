@@ -25,13 +25,13 @@
 // the M-major A operand as they lie in the pages, so no code is ever converted.
 // The B operands are sums of 8-bit parts.  q~: e4m3, 16 times finer each, four for
 // a bf16 output (15 bits or more), six for an f32 one (about 24).  p: e5m2, whose
-// five exponent bits are those of f16.  For a bf16 output p is rounded once to f16
-// and cut exactly into four parts, 8 times finer each; for an f32 one what that
-// rounding left is a second f16 number of four parts (2^-22).  With 2^12 to 2^15
-// for the largest p, a weight down to 2^-26 of it keeps f16's 11 bits, and one is
-// lost only below 2^-37 (2^-49): a key that outweighs a long tail and has a value
-// of nearly nothing leaves the tail its share.  (Three e4m3 parts, a grid of 2^-23
-// of the largest, lost such a tail from 15 nats on.)
+// five exponent bits are those of f16: four parts for a bf16 output, 8 times finer
+// each (2^-12 of p); for an f32 one an f16 number cut into four and what its rounding
+// left cut into four more (2^-22).  With 2^12 to 2^15 for the largest p, a weight
+// down to 2^-25 of it keeps its bits, and one is lost only below 2^-37 (2^-49): a
+// key that outweighs a long tail and has a value of nearly nothing leaves the tail
+// its share.  (Three e4m3 parts, a grid of 2^-23 of the largest, lost such a tail
+// from 15 nats on.)
 // N = parts x heads is 16 to 64 columns; a product of 128 x 128 x N reads 16 KB
 // of A, so the columns cost next to nothing.  (Products on mma.sync f16, with
 // every code converted in registers, left the kernel bound by instructions: 73 us
@@ -566,6 +566,17 @@ constexpr float kPScale = 12.f;     // p is held times 2^12: at most 2^15, below
 // small weights are added to each other before they meet a large one (1.2e-5 off after 256 tiles otherwise).  A bf16 output's rounding covers 2^-10, four thousand tiles of a unit in a block.
 constexpr int kFlush = 16;
 
+// 8 (a - b) of two pairs, exact where a and b are close
+__device__ __forceinline__ float2 eight_times(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, e, n;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 e, {%6, %6};\n\tmov.b64 n, {%7, %7};\n\t"
+      "mul.rn.f32x2 x, x, e;\n\tfma.rn.f32x2 x, y, n, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(8.f), "f"(-8.f));
+  return r;
+}
+
 // the four columns of p's f16 number, each part 8 times finer than the one before
 __device__ __forceinline__ float join_p(const float* v) {
   return fmaf(fmaf(fmaf(v[3], 0.125f, v[2]), 0.125f, v[1]), 0.125f, v[0]);
@@ -1085,10 +1096,12 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
         const float a1 = h + 1 < G ? fast_exp2(x[h + 1] - (ref[h + 1] == -INFINITY ? 0.f : ref[h + 1]) + kPScale) : 0.f;
         l[h] = fmaf(a0, iv, l[h]);
         l[h + 1] = fmaf(a1, iv, l[h + 1]);
-        // two heads as a pair of f16 numbers; the upper byte of one is the e5m2 number that its lower bits are cut off
-        // from, what is left times 8 is exact
-        __half2 p2 = __floats2half2_rn(a0, a1);
-        __half2 rest;                          // what the rounding left, 2^12 times (at most half a step of 2^4)
+        // Two heads as a pair of f16 numbers: the upper byte of one is the e5m2 number that its lower bits are cut off
+        // from, and what is left times 8 is exact.  bf16 outputs: what the first part leaves is taken from the f32 p, so
+        // that f16 rounds an eighth of it, and the others are rounded: off by 2^-12 of p at most, 2^-16 as a rule (an f16
+        // p: 2^-11 and 2^-13).  f32 outputs: all four parts of the f16 p, then of what its rounding left, 2^12 times (at
+        // most half a step of 2^4).
+        __half2 p2 = __floats2half2_rn(a0, a1), rest;
         if (STR == 8) {
           const float2 f = __half22float2(p2);
           rest = __floats2half2_rn((a0 - f.x) * 4096.f, (a1 - f.y) * 4096.f);
@@ -1096,13 +1109,19 @@ __global__ void __launch_bounds__(kThreads, (Cols<STR, NH>::CTAS)) paged_attend_
 #pragma unroll
         for (int i = 0; i < CC::PPARTS; ++i) {
           if (i == 4) p2 = rest;
-          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&p2);
+          uint32_t bits = *reinterpret_cast<const uint32_t*>(&p2);
+          if (STR == 4 && i > 0) bits += 0x00800080u;          // to the nearest, away from 0 on a tie
           const int n0 = h * STR + i, n1 = n0 + STR;
           pb[n0 * TT + ((pchunk ^ (n0 & 7)) << 4)] = (uint8_t)(bits >> 8);
           pb[n1 * TT + ((pchunk ^ (n1 & 7)) << 4)] = (uint8_t)(bits >> 24);
-          if ((i & 3) < 3) {
-            const uint32_t top = bits & 0xff00ff00u;
-            p2 = __hmul2(__hsub2(p2, *reinterpret_cast<const __half2*>(&top)), __float2half2_rn(8.f));
+          const uint32_t top = bits & 0xff00ff00u;
+          const __half2 cut = *reinterpret_cast<const __half2*>(&top);
+          if (STR == 4 && i == 0) {
+            const float2 f = __half22float2(cut);
+            const float2 r = eight_times(make_float2(a0, a1), f);
+            p2 = __floats2half2_rn(r.x, r.y);
+          } else if ((i & 3) < 3) {
+            p2 = __hmul2(__hsub2(p2, cut), __float2half2_rn(8.f));
           }
         }
       }

@@ -434,3 +434,26 @@ def test_decode_parts_of_very_large_scores_keep_their_distance(od):
     assert float((out.double() - want).abs().max()) <= (want * 2.0 ** -8 if od == "bf16" else 1e-5)
     # a sum and a product, each half a step (2^-24) off, and ln 2 in f32 (0.5 * 2^-24)
     assert abs(float(lse) / (np.log(2) * (1.25 * 2 ** 26 + 8 + np.log2(n_pages / 2 * page * (1 + 2.0 ** -8)))) - 1) <= 2.5 * 2.0 ** -24
+
+
+def test_decode_weights_of_bf16_outputs():
+    """One token of weight 2 / (1 + e) and value 1, two of weight 1 and value -1: the output is what two nearly equal sums
+    leave, -e / 2, for 512 values of e.  The weights of a bf16 output are held to 2^-12 of themselves (an f16 number:
+    2^-11, which is most off just above a power of two, where the smaller one lies), its queries to 2^-16."""
+    B, G, page, m, k = 64, 8, 16, 16, 1
+    ck, cv = torch.zeros(1, 1, m, page, dtype=torch.uint8), torch.full((1, 1, page, 128), 0xB8, dtype=torch.uint8)
+    ck[0, 0, 0, 0], cv[0, 0, 0] = 0x38, 0x38
+    cache = pooled(1, B, np.zeros(1, dtype=np.int64), ck, cv)
+    e = np.exp2(np.random.default_rng(103).uniform(-8, -4, (B, G)))
+    q = np.zeros((B, G, 128))
+    q[..., 0] = np.log(2 / (1 + e))
+    q = torch.from_numpy(q).float().cuda()
+    P = torch.eye(128, device="cuda")[None].contiguous()
+    for od in ("bf16", "f32"):
+        out = torch.empty(B, G, 128, dtype=DT[od], device="cuda")
+        ws = torch.full((aq.aqua_paged_decode_workspace_size(cache.desc, G),), 0xFF, dtype=torch.uint8, device="cuda")
+        aq.aqua_paged_decode_attn(cache.desc, q, torch.full((B,), 3, dtype=torch.int32, device="cuda"), P, G, k, out, ws, scale=1.0)
+        w = torch.exp(q[..., :1].double())
+        ref = (w - 2) / (w + 2)
+        tol = 0.5 * (2.0 ** -12 + 2.0 ** -16) + 2.0 ** -8 * ref.abs() if od == "bf16" else 1e-6
+        assert bool(((out.double() - ref).abs() <= tol).all())
