@@ -52,8 +52,8 @@
 //
 // Measured, three launches replayed from a graph: 131072 tokens x 8 heads 58 us
 // (268 MB of rows a head kept: 4.6 TB/s), 32 sequences of up to 32768 tokens, 8
-// heads of 8 queries, 190 to 204 us (4.6 to 5 TB/s), 8 x 8192 tokens 39 us; with f32
-// outputs 63, 329 and 44 us.  With up to
+// heads of 8 queries, 194 us (4.9 TB/s), 8 x 8192 tokens 39.5 us; with f32 outputs
+// 63, 328 and 44 us.  With up to
 // four heads a group the middle of a job is bound by memory (1.5 us a tile and
 // block, two blocks an SM), with eight by the softmax warps' chain of a tile; to
 // that come 9 us until the selection is done and the first scores are there,
